@@ -1,0 +1,72 @@
+// Shared declarations of the many-request operators (packed prompts, paged
+// cache): the kernels' arguments and what a request's lengths mean.
+#pragma once
+
+#include "common.cuh"
+#include "mma_util.cuh"
+
+namespace fl {
+
+constexpr float kPgLog2e = 1.4426950408889634f;
+constexpr float kPgLn2 = 0.6931471805599453f;
+
+struct PgRows {  // 16-bit rows [token, head, head_dim]
+  uint16_t* p;
+  long long st, sh;
+};
+struct PgPages {  // 16-bit pages [page, token, head, head_dim]; packed rows are one page without a table
+  const uint16_t* p;
+  long long sp, st, sh;
+};
+
+struct PgArgs {
+  int B, Hq, Hk, G, max_tokens, max_new;
+  int shift, n_pages, max_blocks;  // page_size = 1 << shift
+  const int32_t* table;            // NULL: keys and values are packed rows
+  const int32_t* kv_lens;          // NULL: a request's cached length is its number of rows
+  const int32_t* cu;
+  PgRows q, o;
+  PgPages k, v;
+  float* lse;
+  int32_t* err;
+  float scale_log2;  // scale * log2(e): scores in log2 units
+};
+
+// Request b: rows [q0, q0 + n) and L columns; n = 0 for one that the call
+// skips (bad lengths are reported).  Row i sees the columns j <= L - n + i.
+struct PgSeq {
+  int q0, n, L;
+};
+__device__ __forceinline__ PgSeq pg_seq(const PgArgs& g, int b) {
+  PgSeq s;
+  const int c0 = g.cu[b], c1 = g.cu[b + 1];
+  s.q0 = c0;
+  s.n = c1 - c0;
+  s.L = g.kv_lens ? g.kv_lens[b] : s.n;
+  bool bad = c0 < 0 || c1 < c0 || c1 > g.max_tokens || s.n > g.max_new || s.L < 0;
+  if (g.table) bad = bad || (long long)s.L > ((long long)g.max_blocks << g.shift);
+  if (bad) {
+    set_error(g.err, FLASHLOOP_DEVERR_INDEX);
+    s.q0 = s.n = s.L = 0;
+  }
+  return s;
+}
+
+// bf16 / fp16 as a template parameter: BF = 1 bf16, 0 fp16.
+template <int BF>
+__device__ __forceinline__ uint32_t pg_pack2(float lo, float hi) {
+  if (BF) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+  return pack_half2(lo, hi);
+}
+template <int BF>
+__device__ __forceinline__ void pg_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (BF) mma_bf16(d, a, b0, b1);
+  else mma_f16(d, a, b0, b1);
+}
+
+int launch_pg_rows(const PgArgs& g, int dh, int bf16, cudaStream_t stream);
+
+}  // namespace fl

@@ -1,0 +1,187 @@
+// C entry points of the many-request operators (see include/flashloop.h):
+// argument checks and launches.
+#include <math.h>
+
+#include "paged.cuh"
+
+namespace fl {
+
+int check_device_arch();
+int launch_paged_plan(const flashloop_paged_params*, int, const int32_t*, const int32_t*, const int32_t*,
+                      const int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*,
+                      cudaStream_t);
+int launch_paged_kv_write(const flashloop_paged_params*, int, const flashloop_rows*, const flashloop_rows*, int,
+                          const int32_t*, const flashloop_pages*, const flashloop_pages*, int32_t*, cudaStream_t);
+
+static int pg_shift(int page_size) {
+  for (int s = 4; s <= 8; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+
+// Sizes that every call reads.
+static int pg_check_sizes(const flashloop_paged_params* p) {
+  if (!p) return FLASHLOOP_ERR_INVALID_ARG;
+  if (p->batch < 0 || p->max_tokens < 0 || p->max_new < 1) return FLASHLOOP_ERR_INVALID_ARG;
+  if (p->batch > 65535) return FLASHLOOP_ERR_UNSUPPORTED;
+  return FLASHLOOP_OK;
+}
+
+static int pg_check_pages(const flashloop_paged_params* p) {
+  if (pg_shift(p->page_size) < 0) return FLASHLOOP_ERR_UNSUPPORTED;
+  if (p->n_pages < 1 || p->max_blocks < 1) return FLASHLOOP_ERR_INVALID_ARG;
+  if ((long long)p->n_pages * p->page_size > 0x7fffffffll || (long long)p->max_blocks * p->page_size > 0x7fffffffll)
+    return FLASHLOOP_ERR_UNSUPPORTED;
+  return FLASHLOOP_OK;
+}
+
+static int pg_check_heads(const flashloop_paged_params* p, bool queries) {
+  if (p->n_kv_heads < 1) return FLASHLOOP_ERR_INVALID_ARG;
+  if (p->head_dim != 64 && p->head_dim != 128) return FLASHLOOP_ERR_UNSUPPORTED;
+  if (p->dtype != FLASHLOOP_DTYPE_BF16 && p->dtype != FLASHLOOP_DTYPE_FP16) return FLASHLOOP_ERR_UNSUPPORTED;
+  if (p->n_kv_heads > 65535) return FLASHLOOP_ERR_UNSUPPORTED;
+  if (!queries) return FLASHLOOP_OK;
+  if (p->n_heads < 1 || p->n_heads % p->n_kv_heads != 0) return FLASHLOOP_ERR_INVALID_ARG;
+  if ((long long)p->max_tokens * p->n_heads > 0x7fffffffll) return FLASHLOOP_ERR_UNSUPPORTED;  // packed rows are 32-bit
+  if (!isfinite(p->scale)) return FLASHLOOP_ERR_INVALID_ARG;
+  return FLASHLOOP_OK;
+}
+
+// Address and strides multiples of 16 bytes; strides not negative.
+static bool pg_aligned(const void* ptr, long long a, long long b, long long c, int elem) {
+  if (!ptr || (reinterpret_cast<uintptr_t>(ptr) & 15) != 0) return false;
+  const long long s[3] = {a, b, c};
+  for (long long x : s)
+    if (x < 0 || x >= (1ll << 36) || (x * elem) % 16 != 0) return false;
+  return true;
+}
+static bool pg_ok(const flashloop_rows* r, int elem) {
+  return r && pg_aligned(r->data, r->stride_token, r->stride_head, 0, elem);
+}
+static bool pg_ok(const flashloop_pages* c) {
+  return c && pg_aligned(c->data, c->stride_page, c->stride_token, c->stride_head, 2);
+}
+
+static PgRows pg_rows(const flashloop_rows* r) {
+  return {static_cast<uint16_t*>(r->data), r->stride_token, r->stride_head};
+}
+static PgPages pg_pages(const flashloop_pages* c) {
+  return {static_cast<const uint16_t*>(c->data), c->stride_page, c->stride_token, c->stride_head};
+}
+
+static PgArgs pg_args(const flashloop_paged_params* p, const flashloop_rows* q, const int32_t* cu,
+                      const flashloop_rows* o, float* lse, int32_t* err) {
+  PgArgs g{};
+  g.B = p->batch;
+  g.Hq = p->n_heads;
+  g.Hk = p->n_kv_heads;
+  g.G = p->n_heads / p->n_kv_heads;
+  g.max_tokens = p->max_tokens;
+  g.max_new = p->max_new < p->max_tokens ? p->max_new : p->max_tokens;
+  g.cu = cu;
+  g.q = pg_rows(q);
+  g.o = pg_rows(o);
+  g.lse = lse;
+  g.err = err;
+  g.scale_log2 = p->scale * kPgLog2e;
+  return g;
+}
+
+}  // namespace fl
+
+using namespace fl;
+
+extern "C" {
+
+int flashloop_paged_plan(const flashloop_paged_params* p, const int32_t* kv_lens, const int32_t* new_lens,
+                         const int32_t* free_pages, const int32_t* n_free, int32_t* block_table, int32_t* cu,
+                         int32_t* kv_lens_out, int32_t* slot_map, int32_t* positions, int32_t* n_free_out,
+                         int32_t* err_word, void* stream) {
+  int rc = pg_check_sizes(p);
+  if (rc == FLASHLOOP_OK) rc = pg_check_pages(p);
+  if (rc != FLASHLOOP_OK) return rc;
+  if (!free_pages || !n_free || !cu || !n_free_out) return FLASHLOOP_ERR_INVALID_ARG;
+  if (p->batch > 0 && (!kv_lens || !new_lens || !block_table || !kv_lens_out)) return FLASHLOOP_ERR_INVALID_ARG;
+  if (p->max_tokens > 0 && (!slot_map || !positions)) return FLASHLOOP_ERR_INVALID_ARG;
+  // every block reads the lengths while block 0 writes the new ones
+  if (n_free == n_free_out) return FLASHLOOP_ERR_INVALID_ARG;
+  if (p->batch > 0 && kv_lens_out < kv_lens + p->batch && kv_lens < kv_lens_out + p->batch)
+    return FLASHLOOP_ERR_INVALID_ARG;
+  if (p->batch > 0 && kv_lens_out < new_lens + p->batch && new_lens < kv_lens_out + p->batch)
+    return FLASHLOOP_ERR_INVALID_ARG;
+  rc = check_device_arch();
+  if (rc != FLASHLOOP_OK) return rc;
+  return launch_paged_plan(p, pg_shift(p->page_size), kv_lens, new_lens, free_pages, n_free, block_table, cu,
+                           kv_lens_out, slot_map, positions, n_free_out, err_word,
+                           reinterpret_cast<cudaStream_t>(stream));
+}
+
+int flashloop_paged_kv_write(const flashloop_paged_params* p, const flashloop_rows* k, const flashloop_rows* v,
+                             int32_t src_dtype, const int32_t* slot_map, const flashloop_pages* k_cache,
+                             const flashloop_pages* v_cache, int32_t* err_word, void* stream) {
+  int rc = pg_check_sizes(p);
+  if (rc == FLASHLOOP_OK) rc = pg_check_pages(p);
+  if (rc == FLASHLOOP_OK) rc = pg_check_heads(p, false);
+  if (rc != FLASHLOOP_OK) return rc;
+  if (src_dtype != FLASHLOOP_DTYPE_FP32 && src_dtype != p->dtype) return FLASHLOOP_ERR_UNSUPPORTED;
+  if (!pg_ok(k_cache) || !pg_ok(v_cache)) return FLASHLOOP_ERR_INVALID_ARG;
+  if (p->max_tokens == 0) return FLASHLOOP_OK;
+  const int elem = src_dtype == FLASHLOOP_DTYPE_FP32 ? 4 : 2;
+  if (!pg_ok(k, elem) || !pg_ok(v, elem) || !slot_map) return FLASHLOOP_ERR_INVALID_ARG;
+  rc = check_device_arch();
+  if (rc != FLASHLOOP_OK) return rc;
+  return launch_paged_kv_write(p, pg_shift(p->page_size), k, v, elem == 4, slot_map, k_cache, v_cache, err_word,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+int flashloop_prompt_attn(const flashloop_paged_params* p, const flashloop_rows* q, const flashloop_rows* k,
+                          const flashloop_rows* v, const int32_t* cu, const flashloop_rows* o, float* lse,
+                          int32_t* err_word, void* stream) {
+  int rc = pg_check_sizes(p);
+  if (rc == FLASHLOOP_OK) rc = pg_check_heads(p, true);
+  if (rc != FLASHLOOP_OK) return rc;
+  if (p->batch == 0 || p->max_tokens == 0) return FLASHLOOP_OK;
+  if (!pg_ok(q, 2) || !pg_ok(k, 2) || !pg_ok(v, 2) || !pg_ok(o, 2) || !cu) return FLASHLOOP_ERR_INVALID_ARG;
+  rc = check_device_arch();
+  if (rc != FLASHLOOP_OK) return rc;
+  PgArgs g = pg_args(p, q, cu, o, lse, err_word);
+  g.k = {static_cast<const uint16_t*>(k->data), 0, k->stride_token, k->stride_head};
+  g.v = {static_cast<const uint16_t*>(v->data), 0, v->stride_token, v->stride_head};
+  return launch_pg_rows(g, p->head_dim, p->dtype == FLASHLOOP_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t flashloop_paged_attn_workspace_bytes(const flashloop_paged_params* p) {
+  if (pg_check_sizes(p) != FLASHLOOP_OK || pg_check_pages(p) != FLASHLOOP_OK ||
+      pg_check_heads(p, true) != FLASHLOOP_OK)
+    return 0;
+  return 256;
+}
+
+int flashloop_paged_attn(const flashloop_paged_params* p, const flashloop_rows* q, const flashloop_pages* k_cache,
+                         const flashloop_pages* v_cache, const int32_t* block_table, const int32_t* kv_lens,
+                         const int32_t* cu, const flashloop_rows* o, float* lse, void* workspace,
+                         size_t workspace_bytes, int32_t* err_word, void* stream) {
+  int rc = pg_check_sizes(p);
+  if (rc == FLASHLOOP_OK) rc = pg_check_pages(p);
+  if (rc == FLASHLOOP_OK) rc = pg_check_heads(p, true);
+  if (rc != FLASHLOOP_OK) return rc;
+  if (!pg_ok(k_cache) || !pg_ok(v_cache)) return FLASHLOOP_ERR_INVALID_ARG;
+  if (p->batch == 0 || p->max_tokens == 0) return FLASHLOOP_OK;
+  if (!pg_ok(q, 2) || !pg_ok(o, 2) || !block_table || !kv_lens || !cu) return FLASHLOOP_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15) != 0 ||
+      workspace_bytes < flashloop_paged_attn_workspace_bytes(p))
+    return FLASHLOOP_ERR_INVALID_ARG;
+  rc = check_device_arch();
+  if (rc != FLASHLOOP_OK) return rc;
+  PgArgs g = pg_args(p, q, cu, o, lse, err_word);
+  g.shift = pg_shift(p->page_size);
+  g.n_pages = p->n_pages;
+  g.max_blocks = p->max_blocks;
+  g.table = block_table;
+  g.kv_lens = kv_lens;
+  g.k = pg_pages(k_cache);
+  g.v = pg_pages(v_cache);
+  return launch_pg_rows(g, p->head_dim, p->dtype == FLASHLOOP_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

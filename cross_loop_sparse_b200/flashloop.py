@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from ctypes import POINTER, c_float, c_int32, c_size_t, c_void_p
+from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 import torch
 
@@ -27,9 +27,9 @@ STATUS = {0: "FLASHLOOP_OK", -1: "FLASHLOOP_ERR_INVALID_ARG", -2: "FLASHLOOP_ERR
 
 
 class FlashLoopError(RuntimeError):
-    def __init__(self, fn, status):
+    def __init__(self, fn, status, detail=""):
         self.status = status
-        super().__init__(f"{fn} returned {status} ({STATUS.get(status, 'unknown')})")
+        super().__init__(f"{fn} returned {status} ({STATUS.get(status, 'unknown')})" + (f": {detail}" if detail else ""))
 
 
 if not os.path.exists(LIB_PATH):
@@ -99,12 +99,43 @@ class DecodeStateC(ctypes.Structure):
                 ("workspace_bytes", c_size_t)]
 
 
+class PagedParams(ctypes.Structure):
+    """Shapes and host-known bounds of the many-request calls (flashloop_paged_params)."""
+    _fields_ = [("batch", c_int32), ("max_tokens", c_int32), ("max_new", c_int32), ("n_heads", c_int32),
+                ("n_kv_heads", c_int32), ("head_dim", c_int32), ("page_size", c_int32), ("n_pages", c_int32),
+                ("max_blocks", c_int32), ("dtype", c_int32), ("scale", c_float)]
+
+    @classmethod
+    def make(cls, batch, max_tokens, max_new, n_heads, n_kv_heads, head_dim, page_size=64, n_pages=1, max_blocks=1,
+             dtype=torch.bfloat16, scale=None):
+        """batch requests with at most max_tokens rows in all and max_new rows each; the page
+        fields matter to the calls that touch the paged cache; scale defaults to 1/sqrt(head_dim)."""
+        if dtype not in PAGED_DTYPES or dtype == torch.float32:
+            raise FlashLoopError("PagedParams.make", -2, f"dtype {dtype}: bfloat16 or float16")
+        return cls(batch, max_tokens, max_new, n_heads, n_kv_heads, head_dim, page_size, n_pages, max_blocks,
+                   PAGED_DTYPES[dtype], head_dim ** -0.5 if scale is None else scale)
+
+
+PAGED_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class RowsC(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("stride_token", c_int64), ("stride_head", c_int64)]
+
+
+class PagesC(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("stride_page", c_int64), ("stride_token", c_int64), ("stride_head", c_int64)]
+
+
 # ----------------------------------------------------------------------------- prototypes
 _P = POINTER(Params)
 _S = POINTER(StateC)
 _D = POINTER(DecodeStateC)
 _V = c_void_p
 _I = c_int32
+_PP = POINTER(PagedParams)
+_RW = POINTER(RowsC)
+_PG = POINTER(PagesC)
 _SIG = {
     "flashloop_workspace_bytes": (c_size_t, [_P]),
     "flashloop_cache_bytes": (c_size_t, [_P, _V]),
@@ -133,6 +164,11 @@ _SIG = {
     "flashloop_check_error_word": (_I, [_V, POINTER(c_int32), _V]),
     "flashloop_selftest_bounded_wait": (_I, [_I, _V, _V]),
     "flashloop_status_string": (ctypes.c_char_p, [_I]),
+    "flashloop_paged_plan": (_I, [_PP, _V, _V, _V, _V, _V, _V, _V, _V, _V, _V, _V, _V]),
+    "flashloop_paged_kv_write": (_I, [_PP, _RW, _RW, _I, _V, _PG, _PG, _V, _V]),
+    "flashloop_prompt_attn": (_I, [_PP, _RW, _RW, _RW, _V, _RW, _V, _V, _V]),
+    "flashloop_paged_attn_workspace_bytes": (c_size_t, [_PP]),
+    "flashloop_paged_attn": (_I, [_PP, _RW, _PG, _PG, _V, _V, _V, _RW, _V, _V, c_size_t, _V, _V]),
 }
 for _name, (_res, _args) in _SIG.items():
     _f = getattr(_lib, _name)
@@ -326,6 +362,120 @@ def flashloop_check_error_word(err_word, stream=None):
     if rc not in (0, -4):
         raise FlashLoopError("flashloop_check_error_word", rc)
     return int(code.value)
+
+
+# ----------------------------------------------------------------------------- many requests
+def _need(ok, fn, detail, status=-1):
+    if not ok:
+        raise FlashLoopError(fn, status, detail)
+
+
+def _vec(fn, name, t, n, dtype, dev):
+    """Address of a contiguous device vector of at least n elements."""
+    if t.dtype != dtype or not t.is_contiguous() or t.numel() < n or t.device != dev:
+        raise FlashLoopError(fn, -1, f"{name}: a contiguous {dtype} tensor of at least {n} elements on {dev}")
+    return t.data_ptr()
+
+
+def _rows(fn, name, t, shape, dtype, dev, written=False):
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        raise FlashLoopError(fn, -1, f"{name}: {dtype} {tuple(shape)} on {dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
+    st, sh, se = t.stride()
+    _need(se == 1, fn, f"{name}: head_dim has to be contiguous")
+    _need(not written or ((st or shape[0] < 2) and (sh or shape[1] < 2)), fn, f"{name}: rows that overlap")
+    return RowsC(t.data_ptr(), st, sh)
+
+
+def _pages(fn, name, t, p, dtype, dev, written=False):
+    shape = (p.n_pages, p.page_size, p.n_kv_heads, p.head_dim)
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        raise FlashLoopError(fn, -1, f"{name}: {dtype} {shape} on {dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
+    st = t.stride()
+    _need(st[3] == 1, fn, f"{name}: head_dim has to be contiguous")
+    _need(not written or all(st[i] or shape[i] < 2 for i in range(3)), fn, f"{name}: pages that overlap")
+    return PagesC(t.data_ptr(), st[0], st[1], st[2])
+
+
+def _paged_dtype(fn, p):
+    _need(p.dtype in (0, 1), fn, "dtype", -2)
+    return torch.float16 if p.dtype else torch.bfloat16
+
+
+def _launch(fn, dev, stream, *args):
+    """Call into the library on the tensors' device, on its current stream by default."""
+    _need(dev.type == "cuda", fn, "tensors on a CUDA device")
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _check(fn, getattr(_lib, fn)(*args, _stream(stream)))
+    return _check(fn, getattr(_lib, fn)(*args, _stream(stream)))
+
+
+def flashloop_paged_plan(params, kv_lens, new_lens, free_pages, n_free, block_table, cu, kv_lens_out, slot_map,
+                         positions, n_free_out, err_word, stream=None):
+    """Block tables, slot maps, positions and packed starts of the tokens that the requests
+    append (see the header).  int32 tensors; block_table [batch, max_blocks] and n_free_out,
+    kv_lens_out, cu [batch + 1], slot_map and positions [max_tokens] are written."""
+    fn, p, dev, i32 = "flashloop_paged_plan", params, kv_lens.device, torch.int32
+    B, T = max(p.batch, 0), max(p.max_tokens, 0)
+    return _launch(fn, dev, stream, ctypes.byref(p), _vec(fn, "kv_lens", kv_lens, B, i32, dev),
+                   _vec(fn, "new_lens", new_lens, B, i32, dev),
+                   _vec(fn, "free_pages", free_pages, 0, i32, dev), _vec(fn, "n_free", n_free, 1, i32, dev),
+                   _vec(fn, "block_table", block_table, B * p.max_blocks, i32, dev),
+                   _vec(fn, "cu", cu, B + 1, i32, dev), _vec(fn, "kv_lens_out", kv_lens_out, B, i32, dev),
+                   _vec(fn, "slot_map", slot_map, T, i32, dev), _vec(fn, "positions", positions, T, i32, dev),
+                   _vec(fn, "n_free_out", n_free_out, 1, i32, dev), _vec(fn, "err_word", err_word, 1, i32, dev))
+
+
+def flashloop_paged_kv_write(params, k, v, slot_map, k_cache, v_cache, err_word, stream=None):
+    """Write k and v [max_tokens, n_kv_heads, head_dim] (params.dtype or float32) into the pages
+    [n_pages, page_size, n_kv_heads, head_dim] of their slots."""
+    fn, p, dev = "flashloop_paged_kv_write", params, k_cache.device
+    dt = _paged_dtype(fn, p)
+    shape = (p.max_tokens, p.n_kv_heads, p.head_dim)
+    _need(k.dtype in PAGED_DTYPES, fn, f"k: {k.dtype}", -2)
+    kr, vr = _rows(fn, "k", k, shape, k.dtype, dev), _rows(fn, "v", v, shape, k.dtype, dev)
+    kc, vc = _pages(fn, "k_cache", k_cache, p, dt, dev, True), _pages(fn, "v_cache", v_cache, p, dt, dev, True)
+    return _launch(fn, dev, stream, ctypes.byref(p), ctypes.byref(kr), ctypes.byref(vr), PAGED_DTYPES[k.dtype],
+                   _vec(fn, "slot_map", slot_map, p.max_tokens, torch.int32, dev), ctypes.byref(kc), ctypes.byref(vc),
+                   _vec(fn, "err_word", err_word, 1, torch.int32, dev))
+
+
+def flashloop_prompt_attn(params, q, k, v, cu, o, lse, err_word, stream=None):
+    """Causal attention over packed prompts: q and o [max_tokens, n_heads, head_dim], k and v
+    [max_tokens, n_kv_heads, head_dim], cu int32 [batch + 1], lse float32 [n_heads, max_tokens] or None."""
+    fn, p, dev = "flashloop_prompt_attn", params, q.device
+    dt = _paged_dtype(fn, p)
+    qs, ks = (p.max_tokens, p.n_heads, p.head_dim), (p.max_tokens, p.n_kv_heads, p.head_dim)
+    qr, kr, vr = _rows(fn, "q", q, qs, dt, dev), _rows(fn, "k", k, ks, dt, dev), _rows(fn, "v", v, ks, dt, dev)
+    orr = _rows(fn, "o", o, qs, dt, dev, True)
+    return _launch(fn, dev, stream, ctypes.byref(p), ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr),
+                   _vec(fn, "cu", cu, p.batch + 1, torch.int32, dev), ctypes.byref(orr),
+                   None if lse is None else _vec(fn, "lse", lse, p.n_heads * p.max_tokens, torch.float32, dev),
+                   _vec(fn, "err_word", err_word, 1, torch.int32, dev))
+
+
+def flashloop_paged_attn_workspace_bytes(params: PagedParams) -> int:
+    return int(_lib.flashloop_paged_attn_workspace_bytes(ctypes.byref(params)))
+
+
+def flashloop_paged_attn(params, q, k_cache, v_cache, block_table, kv_lens, cu, o, lse, workspace, err_word,
+                         stream=None):
+    """Attention of the requests' new rows q [max_tokens, n_heads, head_dim] over their pages
+    (block_table int32 [batch, max_blocks], kv_lens int32 [batch] with the new tokens counted)."""
+    fn, p, dev = "flashloop_paged_attn", params, q.device
+    dt = _paged_dtype(fn, p)
+    qs = (p.max_tokens, p.n_heads, p.head_dim)
+    qr, orr = _rows(fn, "q", q, qs, dt, dev), _rows(fn, "o", o, qs, dt, dev, True)
+    kc, vc = _pages(fn, "k_cache", k_cache, p, dt, dev), _pages(fn, "v_cache", v_cache, p, dt, dev)
+    i32 = torch.int32
+    _need(workspace.is_contiguous() and workspace.device == dev, fn, "workspace: contiguous, on the tensors' device")
+    return _launch(fn, dev, stream, ctypes.byref(p), ctypes.byref(qr), ctypes.byref(kc), ctypes.byref(vc),
+                   _vec(fn, "block_table", block_table, p.batch * p.max_blocks, i32, dev),
+                   _vec(fn, "kv_lens", kv_lens, p.batch, i32, dev), _vec(fn, "cu", cu, p.batch + 1, i32, dev),
+                   ctypes.byref(orr),
+                   None if lse is None else _vec(fn, "lse", lse, p.n_heads * p.max_tokens, torch.float32, dev),
+                   workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                   _vec(fn, "err_word", err_word, 1, i32, dev))
 
 
 # ----------------------------------------------------------------------------- state

@@ -478,6 +478,126 @@ int flashloop_selftest_bounded_wait(int32_t kind, int32_t* err_word, void* strea
 /* Static description of a status code (diagnostics). */
 const char* flashloop_status_string(int status);
 
+/* ---------------------------------------------------------------- many requests: packed prompts, paged cache
+ *
+ * Attention of B requests of different lengths at once, with grouped heads
+ * (query head h reads key head h / (n_heads / n_kv_heads)), in bf16 or fp16.
+ * Interfaces of serving; the paper has no counterpart (its loop runs over one
+ * sequence).  A request's tokens are packed: request b owns rows
+ * [cu[b], cu[b+1]) of q and o.  Its keys and values lie packed alongside
+ * (flashloop_prompt_attn) or in pages of page_size tokens of a shared pool,
+ * where block_table[b, i] is the page of its tokens [i*page_size, (i+1)*page_size)
+ * (flashloop_paged_attn).  A token's slot is page * page_size + position in it.
+ *
+ * Lengths stay on the device; params holds the host-known bounds that size
+ * the grids.  A request whose lengths contradict the bounds (cu not
+ * ascending or beyond max_tokens, more than max_new rows, a cached length
+ * beyond max_blocks pages) sets FLASHLOOP_DEVERR_INDEX and is skipped: its
+ * rows of o and lse are left as they were, as are the rows behind the last
+ * request.  A block-table entry outside [0, n_pages) that a call needs sets
+ * FLASHLOOP_DEVERR_INDEX too; nothing is read through it (its keys and values
+ * count as zero).  Memory behind a request's last cached token is not used,
+ * whatever bits it holds.
+ *
+ * Keys and values that are not finite: a row's result depends on those of the
+ * columns it may see; within a tile of 128 columns a value (not a key) that is
+ * not finite can also reach rows of the same request before it. */
+#define FLASHLOOP_DTYPE_BF16 0
+#define FLASHLOOP_DTYPE_FP16 1
+#define FLASHLOOP_DTYPE_FP32 2
+
+typedef struct flashloop_paged_params {
+  int32_t batch;      /* B >= 0 requests, at most 65535 */
+  int32_t max_tokens; /* rows of q, o, slot_map and positions (cu[B] may be less) */
+  int32_t max_new;    /* bound on the rows of one request, >= 1 */
+  int32_t n_heads;    /* query heads, a multiple of n_kv_heads */
+  int32_t n_kv_heads;
+  int32_t head_dim;   /* 64 or 128 */
+  int32_t page_size;  /* 16, 32, 64, 128 or 256 tokens */
+  int32_t n_pages;    /* pages of the pool; n_pages * page_size < 2^31 */
+  int32_t max_blocks; /* columns of block_table; max_blocks * page_size < 2^31 */
+  int32_t dtype;      /* of q, the cache and o: FLASHLOOP_DTYPE_BF16 or _FP16 */
+  float scale;        /* of q.k, usually 1/sqrt(head_dim) */
+} flashloop_paged_params;
+
+/* Rows [max_tokens, heads, head_dim]: strides in elements, head_dim contiguous.
+ * The address and both strides are multiples of 16 bytes. */
+typedef struct flashloop_rows {
+  void* data;
+  int64_t stride_token;
+  int64_t stride_head;
+} flashloop_rows;
+
+/* A pool of pages [n_pages, page_size, n_kv_heads, head_dim], any order of the
+ * first three (strides in elements; address and strides multiples of 16 bytes). */
+typedef struct flashloop_pages {
+  void* data;
+  int64_t stride_page;
+  int64_t stride_token;
+  int64_t stride_head;
+} flashloop_pages;
+
+/* Block tables and slot maps from request lengths.  Request b holds kv_lens[b]
+ * tokens and appends new_lens[b] >= 0.  free_pages[0..*n_free) is a stack of
+ * free pages; pages are taken from its top, in request order, for the blocks
+ * that the new tokens open:
+ *   cu[b] = sum of new_lens[0..b) (cu[batch] the total),
+ *   kv_lens_out[b] = kv_lens[b] + new_lens[b],
+ *   block_table[b, i] for ceil(kv_lens[b]/page_size) <= i < ceil(kv_lens_out[b]/page_size)
+ *     (other entries are left as they were),
+ *   positions[t] and slot_map[t] of token t of the packed rows; behind the last
+ *     token slot_map is -1 and positions 0, up to max_tokens,
+ *   *n_free_out = *n_free - pages taken.
+ * All or nothing: too few free pages, more than max_tokens tokens or more than
+ * max_blocks blocks set FLASHLOOP_DEVERR_CAPACITY, a negative length or a
+ * count of free pages outside [0, n_pages] FLASHLOOP_DEVERR_INDEX, and then the
+ * call appends nothing: cu is 0, kv_lens_out = kv_lens, *n_free_out = *n_free
+ * and every slot -1.  A page id outside [0, n_pages) on the stack or in the
+ * table sets FLASHLOOP_DEVERR_INDEX and gives its tokens slot -1.  The pages
+ * of a finished request go back by writing them at free_pages[*n_free...).
+ * kv_lens_out and n_free_out do not overlap the inputs. */
+int flashloop_paged_plan(const flashloop_paged_params* p, const int32_t* kv_lens, const int32_t* new_lens,
+                         const int32_t* free_pages, const int32_t* n_free, int32_t* block_table, int32_t* cu,
+                         int32_t* kv_lens_out, int32_t* slot_map, int32_t* positions, int32_t* n_free_out,
+                         int32_t* err_word, void* stream);
+
+/* Write the keys and values of max_tokens rows into the pages of their slots,
+ * rounded to params.dtype (nearest, ties to even).  src_dtype is params.dtype
+ * or FLASHLOOP_DTYPE_FP32 (what flashloop_qkv_gathered leaves).  A row with
+ * slot -1 is skipped; another slot outside [0, n_pages * page_size) sets
+ * FLASHLOOP_DEVERR_INDEX and is skipped.  A finite float32 beyond the largest
+ * fp16 becomes an infinity in an fp16 cache and sets FLASHLOOP_DEVERR_RANGE.
+ * The slots of a call are distinct (plan's are). */
+int flashloop_paged_kv_write(const flashloop_paged_params* p, const flashloop_rows* k, const flashloop_rows* v,
+                             int32_t src_dtype, const int32_t* slot_map, const flashloop_pages* k_cache,
+                             const flashloop_pages* v_cache, int32_t* err_word, void* stream);
+
+/* Causal attention over whole prompts packed end to end.  For row i of request
+ * b (rows counted within the request) and query head h:
+ *   s_j = scale * q_i . k_j for j <= i,  lse = ln sum_j e^(s_j),
+ *   o_i = sum_j e^(s_j - lse) v_j.
+ * k and v are rows of n_kv_heads heads packed as q is.  float32 scores and
+ * sums; the probabilities enter the product with V rounded to the values'
+ * type.  lse: float32 [n_heads, max_tokens], or NULL.  The page fields of
+ * params are not used. */
+int flashloop_prompt_attn(const flashloop_paged_params* p, const flashloop_rows* q, const flashloop_rows* k,
+                          const flashloop_rows* v, const int32_t* cu, const flashloop_rows* o, float* lse,
+                          int32_t* err_word, void* stream);
+
+/* Scratch bytes of flashloop_paged_attn (host function; 0 for bad params). */
+size_t flashloop_paged_attn_workspace_bytes(const flashloop_paged_params* p);
+
+/* Attention of each request's new rows over its cached tokens, the new ones
+ * included (write them first): with n = cu[b+1] - cu[b] and L = kv_lens[b], row i
+ * sees the columns j <= L - n + i.  One row a request is a decode step, more a
+ * chunk of a prompt; requests of a call may differ.  A row that sees no column
+ * gets o = 0 and lse = -inf.  Otherwise as flashloop_prompt_attn.  The scratch
+ * needs no initial value and may be shared by calls that do not overlap. */
+int flashloop_paged_attn(const flashloop_paged_params* p, const flashloop_rows* q, const flashloop_pages* k_cache,
+                         const flashloop_pages* v_cache, const int32_t* block_table, const int32_t* kv_lens,
+                         const int32_t* cu, const flashloop_rows* o, float* lse, void* workspace,
+                         size_t workspace_bytes, int32_t* err_word, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

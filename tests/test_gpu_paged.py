@@ -1,0 +1,344 @@
+"""The many-request operators on the GPU against plain 64-bit implementations:
+block tables and slot maps, cache writes, attention over packed prompts and
+over the paged cache."""
+import math
+import random
+
+import numpy as np
+import pytest
+import torch
+
+from paged_reference import attention, build_plan, gather
+
+F = pytest.importorskip("cross_loop_sparse_b200.flashloop")
+pytestmark = pytest.mark.gpu
+
+BF, HF = torch.bfloat16, torch.float16
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, *shape, dtype=torch.float32, std=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)
+
+
+# ------------------------------------------------------------------------------- plan
+PLANS = [
+    ([0], [1], 16, 0), ([15], [1], 16, 3), ([16], [1], 16, 0), ([0, 0, 0], [0, 0, 0], 64, 5), ([7, 0, 31, 64], [0, 33, 1, 0], 32, 0),
+    ([300], [2000], 128, 17), ([5] * 700, [3] * 700, 16, 1), (list(range(1300)), [i % 5 for i in range(1300)], 256, 40), ([0] * 40, [i * 37 % 900 for i in range(40)], 64, 0),
+]
+
+
+def plan_inputs(held, new, page, pad, seed=0, spare=4):
+    rng = random.Random(seed)
+    blocks = [-(-h // page) for h in held]
+    opened = sum(-(-(h + n) // page) for h, n in zip(held, new)) - sum(blocks)
+    ids = list(range(sum(blocks) + opened + spare))
+    rng.shuffle(ids)
+    width = max(-(-(h + n) // page) for h, n in zip(held, new)) + 2
+    table, at = [], 0
+    for k in blocks:
+        table.append(ids[at:at + k] + [-7] * (width - k))
+        at += k
+    return table, ids[at:], len(ids), width, max(1, sum(new) + pad)
+
+
+class Plan:
+    """Buffers of one call of flashloop_paged_plan."""
+
+    def __init__(self, held, new, table, stack, page, n_pages, width, T):
+        B = len(held)
+        self.p = F.PagedParams.make(batch=B, max_tokens=T, max_new=max(1, max(new, default=1)), n_heads=1, n_kv_heads=1, head_dim=64,
+                                    page_size=page, n_pages=n_pages, max_blocks=width)
+        self.kv, self.new, self.stack = ints(held), ints(new), ints(stack + [-9])
+        self.n_free, self.table = ints([len(stack)]), ints(table)
+        self.cu, self.kv_out, self.slots, self.pos = ints([-3] * (B + 1)), ints([-3] * B), ints([-3] * T), ints([-3] * T)
+        self.n_out, self.err = ints([-3]), ints([0])
+
+    def run(self, stream=None):
+        F.flashloop_paged_plan(self.p, self.kv, self.new, self.stack, self.n_free, self.table, self.cu, self.kv_out, self.slots, self.pos,
+                               self.n_out, self.err, stream)
+        return self
+
+
+@pytest.mark.parametrize("held,new,page,pad", PLANS)
+def test_plan_matches_the_definition(held, new, page, pad):
+    table, stack, n_pages, width, T = plan_inputs(held, new, page, pad)
+    c = Plan(held, new, table, stack, page, n_pages, width, T)
+    for _ in range(2):  # a second call on the same lengths gives the same
+        c.run()
+        cu, kv, tab, slots, pos, left = build_plan(held, new, table, stack, page)
+        spare = T - len(slots)
+        assert c.cu.tolist() == cu and c.kv_out.tolist() == kv and c.n_out.tolist() == [left]
+        assert c.table.tolist() == tab
+        assert c.slots.tolist() == slots + [-1] * spare and c.pos.tolist() == pos + [0] * spare
+        assert c.err.item() == 0
+
+
+@pytest.mark.parametrize("held,new,cut,code", [
+    ([3, 20], [30, 9], "pages", 1), ([3, 20], [30, 9], "tokens", 1), ([3, 20], [30, 9], "blocks", 1), ([3, 20], [30, -1], "", 2), ([-4, 20], [30, 1], "", 2),
+    ([2147483647, 0], [2147483647, 1], "", 1),
+])
+def test_plan_appends_all_or_nothing(held, new, cut, code):
+    page = 16
+    table, stack, n_pages, width, T = plan_inputs([3, 20], [30, 9], page, 0, spare=0)
+    stack = stack[1:] if cut == "pages" else stack
+    T -= cut == "tokens"
+    width = 2 if cut == "blocks" else width
+    table = [r[:width] for r in table]
+    c = Plan(held, new, table, stack, page, n_pages, width, T).run()
+    assert c.err.item() == code
+    assert c.cu.tolist() == [0, 0, 0] and c.kv_out.tolist() == held and c.n_out.tolist() == [len(stack)]
+    assert c.table.tolist() == table
+    assert set(c.slots.tolist()) == {-1} and set(c.pos.tolist()) == {0}
+
+
+def test_plan_reports_bad_pages():
+    table, stack, n_pages, width, T = plan_inputs([3, 20], [30, 9], 16, 0, spare=0)
+    want = build_plan([3, 20], [30, 9], table, stack, 16)[3]
+    bad = stack[-1]
+    c = Plan([3, 20], [30, 9], table, stack[:-1] + [n_pages], 16, n_pages, width, T).run()
+    assert c.err.item() == 2
+    assert c.slots.tolist() == [-1 if s // 16 == bad else s for s in want]
+
+
+# ------------------------------------------------------------------------------- write
+@pytest.mark.parametrize("T,H,dh,src,dt,page,layout", [
+    (1, 1, 64, BF, BF, 16, "thd"), (7, 5, 128, HF, HF, 32, "htd"), (33, 4, 64, torch.float32, BF, 64, "fused"), (130, 3, 128, torch.float32, HF, 256, "thd"),
+    (2001, 8, 128, BF, BF, 128, "fused"),
+])
+def test_write_puts_rows_into_their_slots(T, H, dh, src, dt, page, layout):
+    g = gen(T)
+    n_pages = -(-T // page) + 3
+    if layout == "fused":
+        qkv = randn(g, T, 3 * H, dh, dtype=src)
+        k, v = qkv[:, H:2 * H], qkv[:, 2 * H:]
+    else:
+        k, v = randn(g, T, H, dh, dtype=src), randn(g, T, H, dh, dtype=src)
+    if layout == "htd":  # pages with the heads outside
+        kc, vc = (randn(g, n_pages, H, page, dh, dtype=dt).transpose(1, 2) for _ in range(2))
+    else:
+        both = randn(g, n_pages, 2, page, H, dh, dtype=dt)
+        kc, vc = both[:, 0], both[:, 1]
+    slots = torch.randperm(n_pages * page, generator=g, device="cuda")[:T].to(torch.int32)
+    slots[::5] = -1
+    want_k, want_v = kc.clone(), vc.clone()
+    keep = (slots >= 0).nonzero().flatten()
+    at = slots[keep].long()
+    want_k[at // page, at % page] = k[keep].to(dt)
+    want_v[at // page, at % page] = v[keep].to(dt)
+    p = F.PagedParams.make(batch=1, max_tokens=T, max_new=T, n_heads=H, n_kv_heads=H, head_dim=dh, page_size=page, n_pages=n_pages, dtype=dt)
+    err = ints([0])
+    F.flashloop_paged_kv_write(p, k, v, slots, kc, vc, err)
+    assert torch.equal(kc, want_k) and torch.equal(vc, want_v) and err.item() == 0
+
+
+def test_write_rounds_to_nearest_even_and_reports_range():
+    x = torch.tensor([1 + 2.0 ** -9, 1 + 3 * 2.0 ** -9, 65519.0, -65520.0, math.inf, -math.inf, math.nan, 2.0 ** -26] * 8, device="cuda")
+    for dt, code in ((BF, 0), (HF, 4)):
+        kc, vc = torch.zeros(1, 16, 1, 64, dtype=dt, device="cuda"), torch.zeros(1, 16, 1, 64, dtype=dt, device="cuda")
+        p = F.PagedParams.make(batch=1, max_tokens=1, max_new=1, n_heads=1, n_kv_heads=1, head_dim=64, page_size=16, dtype=dt)
+        err = ints([0])
+        F.flashloop_paged_kv_write(p, x.view(1, 1, 64), torch.zeros(1, 1, 64, device="cuda"), ints([3]), kc, vc, err)
+        assert torch.equal(torch.nan_to_num(kc[0, 3, 0], 7.0), torch.nan_to_num(x.to(dt), 7.0)) and err.item() == code
+    err = ints([0])  # infinities alone are copied without a report
+    F.flashloop_paged_kv_write(p, torch.full((1, 1, 64), math.inf, device="cuda"), torch.zeros(1, 1, 64, device="cuda"), ints([3]), kc, vc, err)
+    assert err.item() == 0
+
+
+def test_write_reports_slots_outside_the_pool():
+    kc, vc = torch.zeros(2, 16, 1, 64, dtype=BF, device="cuda"), torch.zeros(2, 16, 1, 64, dtype=BF, device="cuda")
+    p = F.PagedParams.make(batch=1, max_tokens=4, max_new=4, n_heads=1, n_kv_heads=1, head_dim=64, page_size=16, n_pages=2)
+    k = torch.ones(4, 1, 64, dtype=BF, device="cuda")
+    err = ints([0])
+    F.flashloop_paged_kv_write(p, k, k, ints([32, -2, 31, 2147483647]), kc, vc, err)
+    assert err.item() == 2 and kc.float().sum().item() == 64 and kc[1, 15].float().sum().item() == 64
+
+
+# ------------------------------------------------------------------------------- attention
+def check(got, got_lse, cu, refs, lse, untouched=7.0):
+    for b, (o, l, ot, lt) in enumerate(refs):
+        r = slice(cu[b], cu[b + 1])
+        off = (got[r].double() - o).abs() - ot
+        assert not (off > 0).any() and not got[r].isnan().any(), (b, off.max().item(), (off > 0).sum().item())
+        if lse:
+            empty = l == -math.inf
+            d = got_lse[:, r].double()
+            assert torch.equal(d == -math.inf, empty), b
+            assert ((torch.where(empty, 0.0, d - l).abs() - lt) <= 0).all(), (b, (d - l).abs().max().item())
+    assert (got[cu[-1]:] == untouched).all()
+    if lse:
+        assert (got_lse[:, cu[-1]:] == untouched).all()
+
+
+def starts(n):
+    return [0] + np.cumsum(n).tolist()
+
+
+PROMPTS = [
+    ([1], 1, 1, 64, BF, 0), ([1, 1, 1], 4, 2, 128, HF, 2), ([0, 5, 0, 3, 0], 3, 1, 64, BF, 1), ([127, 128, 129], 4, 4, 128, BF, 0), ([255, 256, 257, 1], 6, 2, 64, HF, 9),
+    ([700, 33, 512], 7, 1, 128, BF, 0), ([1500], 16, 2, 128, HF, 3), ([2049], 2, 2, 64, BF, 0), ([3, 1000, 64, 640], 12, 4, 128, BF, 130), ([300] * 30, 4, 4, 64, HF, 0),
+    ([40] * 200, 8, 1, 128, BF, 0), ([130, 70], 40, 1, 64, BF, 0),
+]
+
+
+@pytest.mark.parametrize("lens,H,Hk,dh,dt,pad", PROMPTS)
+@pytest.mark.parametrize("fused", [False, True])
+def test_prompt_attention(lens, H, Hk, dh, dt, pad, fused):
+    g = gen(len(lens) * 1000 + H)
+    cu = starts(lens)
+    T = max(1, cu[-1] + pad)
+    if fused:
+        qkv = randn(g, T, H + 2 * Hk, dh, dtype=dt, std=1.3)
+        q, k, v = qkv[:, :H], qkv[:, H:H + Hk], qkv[:, H + Hk:]
+        o = torch.full((H, T, dh), 7.0, dtype=dt, device="cuda").transpose(0, 1)
+    else:
+        q, k, v = randn(g, T, H, dh, dtype=dt, std=1.5), randn(g, T, Hk, dh, dtype=dt), randn(g, T, Hk, dh, dtype=dt)
+        o = torch.full((T, H, dh), 7.0, dtype=dt, device="cuda")
+    if pad:
+        k[cu[-1]:], v[cu[-1]:] = math.nan, math.inf
+    lse = torch.full((H, T), 7.0, device="cuda")
+    p = F.PagedParams.make(batch=len(lens), max_tokens=T, max_new=max(lens), n_heads=H, n_kv_heads=Hk, head_dim=dh, dtype=dt)
+    err = ints([0])
+    F.flashloop_prompt_attn(p, q, k, v, ints(cu), o, lse, err)
+    refs = [attention(q[a:b], k[a:b], v[a:b], 0, dh ** -0.5) for a, b in zip(cu, cu[1:])]
+    check(o, lse, cu, refs, True)
+    assert err.item() == 0
+    o2 = torch.full_like(o, 7.0)
+    F.flashloop_prompt_attn(p, q, k, v, ints(cu), o2, None, err)
+    assert torch.equal(o2, o)  # the same bits without the sums, and on a second call
+
+
+def test_prompt_neighbours_do_not_leak():
+    """Infinities and NaN in one request's rows stay in that request."""
+    g, lens = gen(5), [200, 77, 300, 131]
+    cu = starts(lens)
+    T, H, Hk, dh = cu[-1], 4, 2, 128
+    q, k, v = randn(g, T, H, dh, dtype=BF), randn(g, T, Hk, dh, dtype=BF), randn(g, T, Hk, dh, dtype=BF)
+    for x in (q, k, v):
+        x[cu[1]:cu[2]] = math.nan
+        x[cu[3] + 3] = math.inf
+    p = F.PagedParams.make(batch=4, max_tokens=T, max_new=300, n_heads=H, n_kv_heads=Hk, head_dim=dh)
+    o, lse, err = torch.empty(T, H, dh, dtype=BF, device="cuda"), torch.empty(H, T, device="cuda"), ints([0])
+    F.flashloop_prompt_attn(p, q, k, v, ints(cu), o, lse, err)
+    for b in (0, 2):
+        r = slice(cu[b], cu[b + 1])
+        want, l, ot, lt = attention(q[r], k[r], v[r], 0, dh ** -0.5)
+        assert ((o[r].double() - want).abs() <= ot).all() and ((lse[:, r].double() - l).abs() <= lt).all()
+    assert o[cu[1]:cu[2]].isnan().all()
+
+
+PAGED = [  # cached lengths (new tokens included), new tokens, H, Hk, dh, page, type, layout, pad
+    ([1], [1], 1, 1, 64, 16, BF, "thd", 0),
+    ([256], [1], 4, 4, 64, 16, BF, "thd", 0),
+    ([5, 0, 300, 16, 17], [1, 1, 1, 0, 1], 8, 2, 128, 16, HF, "thd", 1),
+    ([4000, 63, 64, 65, 1], [1] * 5, 16, 16, 128, 64, BF, "htd", 2),
+    ([9000], [1], 8, 1, 128, 32, BF, "both", 0),
+    ([20000, 3], [1, 1], 2, 1, 64, 256, HF, "thd", 0),
+    ([700, 41, 2000], [3, 4, 2], 7, 1, 128, 16, BF, "thd", 0),
+    ([700, 41, 2000], [4, 4, 4], 8, 1, 64, 128, HF, "both", 3),
+    ([130, 600], [130, 17], 4, 2, 128, 16, BF, "thd", 0),
+    ([1000, 257, 128], [300, 257, 5], 12, 4, 128, 64, HF, "htd", 4),
+    ([5000], [64], 8, 2, 64, 32, BF, "thd", 0),
+    ([4100, 6000], [100, 333], 32, 8, 128, 64, BF, "both", 0),
+    ([2000, 900, 3, 400, 1], [1, 500, 1, 37, 1], 16, 2, 128, 32, BF, "thd", 7),
+    ([3, 2, 100, 9], [8, 2, 300, 40], 4, 1, 128, 16, BF, "thd", 0),       # fewer cached than new: rows that see nothing
+    ([0, 0], [1, 200], 4, 2, 64, 16, HF, "thd", 0),
+    ([513] * 70, [1] * 70, 4, 1, 128, 16, BF, "thd", 0),
+    ([300] * 64, [9] * 64, 6, 2, 64, 64, HF, "thd", 0),
+    ([900, 900], [1, 1], 40, 1, 128, 128, BF, "thd", 0),                   # more heads a group than a tile of the few-row kernel
+]
+
+
+def paged_inputs(total, new, H, Hk, dh, page, dt, layout, pad, seed=0):
+    g = gen(seed + sum(total) + H)
+    blocks = [-(-t // page) for t in total]
+    n_pages, width = sum(blocks) + 2, max(1, max(blocks)) + 1
+    order = torch.randperm(n_pages, generator=g, device="cuda").to(torch.int32)
+    table = torch.full((len(total), width), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, k in enumerate(blocks):
+        table[b, :k] = order[at:at + k]
+        at += k
+    if layout == "htd":
+        kc, vc = (randn(g, n_pages, Hk, page, dh, dtype=dt).transpose(1, 2) for _ in range(2))
+    elif layout == "both":
+        both = randn(g, n_pages, 2, page, Hk, dh, dtype=dt)
+        kc, vc = both[:, 0], both[:, 1]
+    else:
+        kc, vc = randn(g, n_pages, page, Hk, dh, dtype=dt), randn(g, n_pages, page, Hk, dh, dtype=dt)
+    # bits of earlier owners behind every request's last token, and in the pages that nobody holds
+    for b, t in enumerate(total):
+        if t % page:
+            kc[table[b, t // page].long(), t % page:], vc[table[b, t // page].long(), t % page:] = math.nan, math.inf
+    kc[order[at:].long()], vc[order[at:].long()] = math.nan, math.nan
+    cu = starts(new)
+    T = max(1, cu[-1] + pad)
+    q = randn(g, T, H, dh, dtype=dt, std=1.5)
+    p = F.PagedParams.make(batch=len(total), max_tokens=T, max_new=max(1, max(new)), n_heads=H, n_kv_heads=Hk, head_dim=dh, page_size=page,
+                           n_pages=n_pages, max_blocks=width, dtype=dt)
+    return p, q, kc, vc, table, cu
+
+
+def workspace(p):
+    return torch.full((F.flashloop_paged_attn_workspace_bytes(p),), 0xA5, dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("total,new,H,Hk,dh,page,dt,layout,pad", PAGED)
+def test_paged_attention(total, new, H, Hk, dh, page, dt, layout, pad):
+    p, q, kc, vc, table, cu = paged_inputs(total, new, H, Hk, dh, page, dt, layout, pad)
+    o, lse, err, ws = torch.full_like(q, 7.0), torch.full((H, q.shape[0]), 7.0, device="cuda"), ints([0]), workspace(p)
+    F.flashloop_paged_attn(p, q, kc, vc, table, ints(total), ints(cu), o, lse, ws, err)
+    refs = [attention(q[cu[b]:cu[b + 1]], gather(kc, table[b], t), gather(vc, table[b], t), t - new[b], dh ** -0.5) for b, t in enumerate(total)]
+    check(o, lse, cu, refs, True)
+    assert err.item() == 0
+    o2 = torch.full_like(q, 7.0)
+    F.flashloop_paged_attn(p, q, kc, vc, table, ints(total), ints(cu), o2, None, ws, err)
+    assert torch.equal(o2, o)
+
+
+def test_paged_attention_equals_prompt_attention():
+    """A whole prompt as one chunk over an empty cache is the prompt's own attention."""
+    p, q, kc, vc, table, cu = paged_inputs([700, 130], [700, 130], 8, 2, 128, 64, BF, "thd", 0)
+    k = torch.cat([gather(kc, table[b], t) for b, t in enumerate((700, 130))])
+    v = torch.cat([gather(vc, table[b], t) for b, t in enumerate((700, 130))])
+    a, b, err = torch.empty_like(q), torch.empty_like(q), ints([0])
+    F.flashloop_paged_attn(p, q, kc, vc, table, ints([700, 130]), ints(cu), a, None, workspace(p), err)
+    F.flashloop_prompt_attn(p, q, k, v, ints(cu), b, None, err)
+    r = attention(q[:700], k[:700], v[:700], 0, 128 ** -0.5)
+    assert ((a[:700].double() - r[0]).abs() <= r[2]).all() and ((a.double() - b.double()).abs()[:700] <= 2 * r[2]).all()
+
+
+@pytest.mark.parametrize("new", [1, 200])
+def test_paged_attention_reports_bad_pages_and_lengths(new):
+    total = [900, 700, 800]
+    p, q, kc, vc, table, cu = paged_inputs(total, [new] * 3, 4, 2, 128, 16, BF, "thd", 0)
+    table[1, 3], table[2, 5] = p.n_pages, -1
+    o, err, ws = torch.full_like(q, 7.0), ints([0]), workspace(p)
+    F.flashloop_paged_attn(p, q, kc, vc, table, ints(total), ints(cu), o, None, ws, err)
+    assert err.item() == 2
+    r = attention(q[:new], gather(kc, table[0], 900), gather(vc, table[0], 900), 900 - new, 128 ** -0.5)
+    assert ((o[:new].double() - r[0]).abs() <= r[2]).all()
+    # the bad page's keys and values count as zero
+    k, v = kc.clone(), vc.clone()
+    tab = table.clone()
+    tab[1, 3] = table[0, 0]
+    kk, vv = gather(k, tab[1], 700), gather(v, tab[1], 700)
+    kk[48:64], vv[48:64] = 0, 0
+    r = attention(q[new:2 * new], kk, vv, 700 - new, 128 ** -0.5)
+    assert ((o[new:2 * new].double() - r[0]).abs() <= r[2]).all()
+    # a length beyond the table, starts that descend and a negative length skip their requests only
+    table[1, 3], table[2, 5] = 0, 0
+    for lens, c in (([900, table.shape[1] * 16 + 1, 800], cu), ([900, -1, 800], cu), ([900, 700, 800], [0, new, new - 1, 3 * new])):
+        o, err = torch.full_like(q, 7.0), ints([0])
+        F.flashloop_paged_attn(p, q, kc, vc, table, ints(lens), ints(c), o, None, ws, err)
+        assert err.item() == 2 and (o[:new] != 7).any() and not (o[:new] == 7).all(2).any()
+        assert c is not cu or (o[new:2 * new] == 7).all()
