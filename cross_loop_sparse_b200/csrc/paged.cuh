@@ -29,7 +29,8 @@ struct PgArgs {
   PgPages k, v;
   float* lse;
   int32_t* err;
-  float scale_log2;  // scale * log2(e): scores in log2 units
+  float scale_log2;  // scale * log2(e) > 0: scores in log2 units
+  int skip_longer;   // requests with more than max_new rows are another kernel's, not a fault
 };
 
 // Request b: rows [q0, q0 + n) and L columns; n = 0 for one that the call
@@ -43,12 +44,13 @@ __device__ __forceinline__ PgSeq pg_seq(const PgArgs& g, int b) {
   s.q0 = c0;
   s.n = c1 - c0;
   s.L = g.kv_lens ? g.kv_lens[b] : s.n;
-  bool bad = c0 < 0 || c1 < c0 || c1 > g.max_tokens || s.n > g.max_new || s.L < 0;
+  bool bad = c0 < 0 || c1 < c0 || c1 > g.max_tokens || (s.n > g.max_new && !g.skip_longer) || s.L < 0;
   if (g.table) bad = bad || (long long)s.L > ((long long)g.max_blocks << g.shift);
   if (bad) {
     set_error(g.err, FLASHLOOP_DEVERR_INDEX);
     s.q0 = s.n = s.L = 0;
   }
+  if (g.skip_longer && s.n > g.max_new) s.n = 0;
   return s;
 }
 
@@ -67,6 +69,21 @@ __device__ __forceinline__ void pg_mma(float (&d)[4], const uint32_t (&a)[4], ui
   else mma_f16(d, a, b0, b1);
 }
 
+// The scratch of the paged attention.  A block that takes a cut of the column
+// line holds at most two items that are not whole, the first and the last.
+constexpr int kPgSms = 148;  // blocks of the tile kernel at most
+struct PgScratch {
+  uint32_t* tile_tickets;  // [2 * kPgSms * 2] arrivals of an item's parts, zeroed by the call
+  float2* tile_mz;         // [2 * kPgSms, 256] (m, z)
+  float* tile_n;           // [2 * kPgSms, 256, head_dim]
+  size_t ticket_bytes, total;
+};
+
+// Requests of at most this many packed rows (rows x group) are the few-row
+// kernel's, which reads the cache once for 32 of them; longer ones the tile kernel's.
+constexpr int kPgFewRows = 32;
+
 int launch_pg_rows(const PgArgs& g, int dh, int bf16, cudaStream_t stream);
+int launch_pg_tile(const PgArgs& g, int dh, int bf16, int few, const PgScratch& ws, cudaStream_t stream);
 
 }  // namespace fl

@@ -43,7 +43,7 @@ static int pg_check_heads(const flashloop_paged_params* p, bool queries) {
   if (!queries) return FLASHLOOP_OK;
   if (p->n_heads < 1 || p->n_heads % p->n_kv_heads != 0) return FLASHLOOP_ERR_INVALID_ARG;
   if ((long long)p->max_tokens * p->n_heads > 0x7fffffffll) return FLASHLOOP_ERR_UNSUPPORTED;  // packed rows are 32-bit
-  if (!isfinite(p->scale)) return FLASHLOOP_ERR_INVALID_ARG;
+  if (!isfinite(p->scale) || !(p->scale > 0.f)) return FLASHLOOP_ERR_INVALID_ARG;
   return FLASHLOOP_OK;
 }
 
@@ -67,6 +67,33 @@ static PgRows pg_rows(const flashloop_rows* r) {
 }
 static PgPages pg_pages(const flashloop_pages* c) {
   return {static_cast<const uint16_t*>(c->data), c->stride_page, c->stride_token, c->stride_head};
+}
+
+// TMA takes no stride of zero (rows that a caller broadcast); the few-row
+// kernel's own loads do, whatever the number of rows.
+static bool pg_tma_ok(const PgArgs& g, int pages) {
+  for (const PgPages* t : {&g.k, &g.v})
+    if (t->st == 0 || (g.Hk > 1 && t->sh == 0) || (pages > 1 && t->sp == 0)) return false;
+  return true;
+}
+
+// Offsets depend on the shape alone.
+static PgScratch pg_scratch(const flashloop_paged_params* p, void* base) {
+  PgScratch w{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  const size_t slots = 2 * kPgSms;
+  const bool tiles = (long long)p->max_new * (p->n_heads / p->n_kv_heads) > kPgFewRows;
+  w.ticket_bytes = slots * 2 * sizeof(uint32_t);
+  w.tile_tickets = ws_ptr<uint32_t>(base, take(w.ticket_bytes));
+  w.tile_mz = ws_ptr<float2>(base, take(tiles ? slots * 256 * sizeof(float2) : 0));
+  w.tile_n = ws_ptr<float>(base, take(tiles ? slots * 256 * (size_t)p->head_dim * sizeof(float) : 0));
+  w.total = off;
+  return w;
 }
 
 static PgArgs pg_args(const flashloop_paged_params* p, const flashloop_rows* q, const int32_t* cu,
@@ -147,14 +174,17 @@ int flashloop_prompt_attn(const flashloop_paged_params* p, const flashloop_rows*
   PgArgs g = pg_args(p, q, cu, o, lse, err_word);
   g.k = {static_cast<const uint16_t*>(k->data), 0, k->stride_token, k->stride_head};
   g.v = {static_cast<const uint16_t*>(v->data), 0, v->stride_token, v->stride_head};
-  return launch_pg_rows(g, p->head_dim, p->dtype == FLASHLOOP_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream));
+  const int bf16 = p->dtype == FLASHLOOP_DTYPE_BF16;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!pg_tma_ok(g, 1)) return launch_pg_rows(g, p->head_dim, bf16, s);
+  return launch_pg_tile(g, p->head_dim, bf16, 0, PgScratch{}, s);
 }
 
 size_t flashloop_paged_attn_workspace_bytes(const flashloop_paged_params* p) {
   if (pg_check_sizes(p) != FLASHLOOP_OK || pg_check_pages(p) != FLASHLOOP_OK ||
       pg_check_heads(p, true) != FLASHLOOP_OK)
     return 0;
-  return 256;
+  return pg_scratch(p, nullptr).total;
 }
 
 int flashloop_paged_attn(const flashloop_paged_params* p, const flashloop_rows* q, const flashloop_pages* k_cache,
@@ -181,7 +211,22 @@ int flashloop_paged_attn(const flashloop_paged_params* p, const flashloop_rows* 
   g.kv_lens = kv_lens;
   g.k = pg_pages(k_cache);
   g.v = pg_pages(v_cache);
-  return launch_pg_rows(g, p->head_dim, p->dtype == FLASHLOOP_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream));
+  const int bf16 = p->dtype == FLASHLOOP_DTYPE_BF16;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool tiles = (long long)g.max_new * g.G > kPgFewRows && pg_tma_ok(g, p->n_pages);
+  const PgScratch ws = pg_scratch(p, workspace);
+  if (tiles) {
+    FL_TRY(cudaMemsetAsync(ws.tile_tickets, 0, ws.ticket_bytes, s));
+    PgArgs few = g;
+    few.max_new = kPgFewRows / g.G;
+    few.skip_longer = 1;
+    if (few.max_new > 0) {
+      rc = launch_pg_rows(few, p->head_dim, bf16, s);
+      if (rc != FLASHLOOP_OK) return rc;
+    }
+    return launch_pg_tile(g, p->head_dim, bf16, kPgFewRows, ws, s);
+  }
+  return launch_pg_rows(g, p->head_dim, bf16, s);
 }
 
 }  // extern "C"

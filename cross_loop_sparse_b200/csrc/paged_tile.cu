@@ -1,0 +1,807 @@
+// Attention of many packed rows over many columns (tcgen05): packed prompts
+// and chunks of new tokens over a paged cache.
+//
+// The rows of a request and key head are packed token-major, r = token * G +
+// (query head within the group): grouped heads fill a tile with rows that
+// read the same keys.  Work item: one request, key head and pair of 128-row
+// tiles A, B, over a range of 128-column tiles; A and B share every K / V
+// tile.  Per row, with s the scores in log2 units and m a reference raised
+// only when a score exceeds it by 8,
+//   p = 2^(s - m), z = sum p, N = sum p v, o = N / z, lse = (m + log2 z) ln 2;
+// scores, z and N in float32, p rounded to the values' type because the
+// matrix product takes one type for both operands.
+//
+// Shared memory: the pair's queries (2 x 128 x DH) and a ring of K / V slots of
+// 128 columns (K-major K tiles; V as it lies in memory, MN-major), all in the
+// 128-byte swizzle.  K and V come by TMA: one box of 128 tokens of packed rows
+// or of a page, or one box a page where pages are smaller.  Boxes of pages
+// behind the request's end start outside the tensor and fill with zeros; the
+// V rows behind the end of the last tile are cleared before the tile is
+// handed on, since 0 * NaN would reach the rows.
+// TMEM (512 columns): N_A, N_B, then the tiles' 128-column scores; the P of a
+// 64-column half is written over the half's first 32 score columns and feeds
+// that half's P.V from TMEM.  The score MMA is 128 wide (two 64-wide ones read
+// the queries twice and are bound by shared memory).
+//
+// Roles (16 warps): 0-3 / 4-7 rows of tile A / B, one thread a row; 8-11
+// queries of the next item; 12 TMEM and K / V loads (lane = page of a tile);
+// 13 / 14 MMA issue of tile A / B; 15 work items.  While one tile's rows take
+// their exponentials the other tile's MMAs run.  A quarter of the exponentials
+// of unmasked halves is taken by polynomial on the FMA units: MUFU's 16 a
+// clock would need as long for a tile as its MMAs do.
+//
+// Work: without scratch (prompts) an item is a whole row pair, long ones first
+// within a head.  With scratch (paged) the column tiles of all items are one
+// line that is cut into equal lengths, one a block, so that few rows over a
+// long cache still use every SM; an item cut by a border is joined by the
+// block that finishes last (float32 N, m, z in scratch, in the order of its
+// parts, so that results do not depend on timing).
+//
+// Every wait is bounded; one that gives up sets FLASHLOOP_DEVERR_TIMEOUT and
+// the block unwinds.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <type_traits>
+
+#include "paged.cuh"
+#include "tc_util.cuh"
+
+namespace fl {
+
+constexpr int kPtRows = 128;
+constexpr int kPtPair = 2 * kPtRows;
+constexpr int kPtCols = 128;
+constexpr int kPtThreads = 512;
+constexpr int kPtWarpQ = 8, kPtWarpTma = 12, kPtWarpMma = 13, kPtWarpSched = 15;
+constexpr float kPtRescale = 8.f;
+constexpr int kPtReaders = 15;   // arrivals that free a work item's slot: 8 + 4 + 1 + 2 warps
+constexpr int kPtMinUnits = 4;   // column tiles a block takes at least when the line is cut
+
+template <int DH>
+struct PtCfg {
+  static constexpr int kQChunk = kPtRows * 128;
+  static constexpr int kQBytes = kPtRows * DH * 2;
+  static constexpr int kChunk = kPtCols * 128;  // 128 tokens x 64 elements
+  static constexpr int kSlotBytes = kPtCols * DH * 2;
+  static constexpr int kStages = DH == 128 ? 5 : 8;
+  static constexpr int kRingOff = 2 * kQBytes;
+  static constexpr int kBarOff = kRingOff + kStages * kSlotBytes;
+  static constexpr int kSmem = 1024 + kBarOff + 512;
+  static_assert(kSmem <= 232448, "shared memory per block");
+};
+
+struct PtItem {
+  int valid, b, h, q0, n, L, r0;
+  int t0, t1;            // column tiles
+  int slot, slot0, parts, part;  // scratch slot of this part, of part 0, number of parts (1 = whole)
+};
+
+struct PtArgs {
+  PgArgs g;
+  int few;        // requests with at most this many packed rows are another kernel's
+  int box_shift;  // tokens of a TMA box: 1 << box_shift
+  uint32_t* tickets;  // [2 * grid * 2], zero; NULL: items are whole
+  float2* part_mz;    // [2 * grid, 256]
+  float* part_n;      // [2 * grid, 256, DH]
+};
+
+__device__ __forceinline__ int pt_pairs(const PtArgs& a, int n) {
+  const int rows = n * a.g.G;
+  return rows <= a.few ? 0 : (rows + kPtPair - 1) / kPtPair;
+}
+// Column tiles that the rows before packed row `end` see.
+__device__ __forceinline__ int pt_tiles(int n, int L, int G, int end) {
+  const int f = L - n + (min(end, n * G) - 1) / G + 1;
+  return f > 0 ? (f + kPtCols - 1) / kPtCols : 0;
+}
+// Column tiles of pair p; a pair that sees none still has its rows written.
+__device__ __forceinline__ int pt_units(int n, int L, int G, int p) {
+  return max(1, pt_tiles(n, L, G, (p + 1) * kPtPair));
+}
+
+// Warp 15: cuts the work into items.  `emit` returns false when the block ends.
+template <typename Emit>
+__device__ __forceinline__ void pt_schedule(const PtArgs& a, int lane, Emit emit) {
+  const PgArgs& g = a.g;
+  const int G = g.G;
+  constexpr unsigned kAll = 0xffffffffu;
+  // lane's request of the chunk at b0, and its pairs
+  PgSeq s;
+  int np;
+  auto chunk = [&](int b0) {
+    s = {0, 0, 0};
+    if (b0 + lane < g.B) s = pg_seq(g, b0 + lane);
+    np = pt_pairs(a, s.n);
+  };
+  if (a.tickets == nullptr) {
+    // whole items, block i takes items i, i + grid, ...
+    long long item = blockIdx.x, base = 0;
+    for (int b0 = 0; b0 < g.B; b0 += 32) {
+      chunk(b0);
+      const long long mine = (long long)np * g.Hk;
+      long long end = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(kAll, end, o);
+        if (lane >= o) end += y;
+      }
+      const long long total = __shfl_sync(kAll, end, 31);
+      while (item < base + total) {
+        const int src = __ffs(__ballot_sync(kAll, base + end > item)) - 1;
+        const int n_p = __shfl_sync(kAll, np, src);
+        const long long idx = item - base - __shfl_sync(kAll, end - mine, src);
+        PtItem it{};
+        it.valid = 1;
+        it.b = b0 + src;
+        it.h = (int)(idx / n_p);
+        it.q0 = __shfl_sync(kAll, s.q0, src);
+        it.n = __shfl_sync(kAll, s.n, src);
+        it.L = __shfl_sync(kAll, s.L, src);
+        const int p = n_p - 1 - (int)(idx % n_p);  // long rows first
+        it.r0 = p * kPtPair;
+        it.t1 = pt_tiles(it.n, it.L, G, it.r0 + kPtPair);
+        it.parts = 1;
+        if (!emit(it)) return;
+        item += gridDim.x;
+      }
+      base += total;
+    }
+    return;
+  }
+  // column tiles of one key head of the lane's request (of the chunk loaded last)
+  auto head_units = [&]() -> long long {
+    long long u = 0;
+    if (np <= 8)
+      for (int p = 0; p < np; ++p) u += pt_units(s.n, s.L, G, p);
+    unsigned big = __ballot_sync(kAll, np > 8);
+    while (big) {
+      const int src = __ffs(big) - 1;
+      big &= big - 1;
+      const int n_p = __shfl_sync(kAll, np, src), n = __shfl_sync(kAll, s.n, src), L = __shfl_sync(kAll, s.L, src);
+      long long v = 0;
+      for (int p = lane; p < n_p; p += 32) v += pt_units(n, L, G, p);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+      if (lane == src) u = v;
+    }
+    return u;
+  };
+  long long total = 0;
+  for (int b0 = 0; b0 < g.B; b0 += 32) {
+    chunk(b0);
+    long long u = head_units() * g.Hk;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(kAll, u, o);
+    total += u;
+  }
+  const long long per = max((long long)kPtMinUnits, (total + gridDim.x - 1) / gridDim.x);
+  long long x = blockIdx.x * per;
+  const long long x1 = min(total, x + per);
+  long long base = 0;
+  for (int b0 = 0; b0 < g.B && x < x1; b0 += 32) {
+    chunk(b0);
+    const long long hu = head_units(), mine = hu * g.Hk;
+    long long end = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(kAll, end, o);
+      if (lane >= o) end += y;
+    }
+    const long long chunk_total = __shfl_sync(kAll, end, 31);
+    while (x < x1 && x < base + chunk_total) {
+      const int src = __ffs(__ballot_sync(kAll, base + end > x)) - 1;
+      const int n_p = __shfl_sync(kAll, np, src);
+      const long long head = __shfl_sync(kAll, hu, src);
+      const long long b_at = base + __shfl_sync(kAll, end - mine, src);  // the request's first unit
+      PtItem it{};
+      it.valid = 1;
+      it.b = b0 + src;
+      it.q0 = __shfl_sync(kAll, s.q0, src);
+      it.n = __shfl_sync(kAll, s.n, src);
+      it.L = __shfl_sync(kAll, s.L, src);
+      it.h = (int)((x - b_at) / head);
+      long long at = b_at + it.h * head;  // the head's first unit; pairs follow, long rows first
+      // the pair that holds x: prefix sums over 32 pairs at a time
+      for (int i0 = 0; i0 < n_p; i0 += 32) {
+        const int i = i0 + lane;
+        const int u = i < n_p ? pt_units(it.n, it.L, G, n_p - 1 - i) : 0;
+        long long e = u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(kAll, e, o);
+          if (lane >= o) e += y;
+        }
+        const unsigned hit = __ballot_sync(kAll, at + e > x);
+        if (hit == 0) {
+          at += __shfl_sync(kAll, e, 31);
+          continue;
+        }
+        const int hl = __ffs(hit) - 1;
+        const long long u1 = at + __shfl_sync(kAll, e, hl), u0 = u1 - __shfl_sync(kAll, u, hl);
+        it.r0 = (n_p - 1 - (i0 + hl)) * kPtPair;
+        it.t0 = (int)(x - u0);
+        it.t1 = (int)(min(u1, x1) - u0);
+        const long long fc = u0 / per, lc = (u1 - 1) / per;
+        it.parts = (int)(lc - fc) + 1;
+        it.part = (int)(blockIdx.x - fc);
+        it.slot0 = (int)(fc * 2 + (u0 % per != 0));
+        it.slot = it.part == 0 ? it.slot0 : (int)(blockIdx.x * 2);
+        x = min(u1, x1);
+        break;
+      }
+      // a pair that sees no column has one unit and no tiles
+      it.t1 = min(it.t1, pt_tiles(it.n, it.L, G, it.r0 + kPtPair));
+      if (!emit(it)) return;
+    }
+    base += chunk_total;
+  }
+}
+
+// Column tiles of the item that tile x (0 = A, 1 = B) reads, from t0 on.
+__device__ __forceinline__ int pt_mine(const PtItem& it, int G, int x) {
+  const int first = it.r0 + x * kPtRows;
+  if (first >= it.n * G) return 0;
+  return max(0, min(it.t1, pt_tiles(it.n, it.L, G, first + kPtRows)) - it.t0);
+}
+
+template <int DH, int BF>
+__global__ void __launch_bounds__(kPtThreads, 1)
+pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, PtArgs a) {
+  using C = PtCfg<DH>;
+  constexpr uint32_t kIdescS = f16_idesc(128, 128, BF);
+  constexpr uint32_t kIdescPV = f16_idesc(128, DH, BF) | kIdescBMnMajor;
+  constexpr uint32_t kColS = 256;  // tile x: scores at 256 + 128 x, numerator at x * DH
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* kv_full = bars;                  // [stages] a slot's bytes landed
+  uint64_t* kv_empty = bars + C::kStages;    // [stages] both issuers done with the slot
+  uint64_t* s_full = bars + 2 * C::kStages;  // [x] scores of a column tile in TMEM
+  uint64_t* p_full = s_full + 2;             // [x * 2 + half] P of a half written (128 threads)
+  uint64_t* pv_done = p_full + 4;            // [x] a half's P.V completed (two a column tile)
+  uint64_t* acc_full = pv_done + 2;          // [x] the item's last P.V completed
+  uint64_t* n_free = acc_full + 2;           // [x] the numerator has been read (128 threads)
+  uint64_t* q_full = n_free + 2;             // [x] queries stored (128 threads)
+  uint64_t* q_empty = q_full + 2;            // [x] the item's score MMAs completed
+  uint64_t* item_full = q_empty + 2;         // [2]
+  uint64_t* item_empty = item_full + 2;      // [2]
+  uint64_t* tail = item_empty + 2;           // [1] bytes of a V tile whose last rows are cleared
+  uint64_t* fin = tail + 1;                  // [1] every MMA of both issuers completed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* last_flag = reinterpret_cast<int*>(tmem_slot + 2);  // [x]
+  PtItem* items = reinterpret_cast<PtItem*>(tmem_slot + 4);  // [2]
+  static_assert((2 * C::kStages + 24) * 8 + 16 + 2 * sizeof(PtItem) <= 512, "barriers");
+  uint8_t* ring = smem + C::kRingOff;
+  const PgArgs& g = a.g;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 2);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], kPtRows);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&pv_done[x], 1);
+      mbar_init(&acc_full[x], 1);
+      mbar_init(&n_free[x], kPtRows);
+      mbar_init(&q_full[x], kPtRows);
+      mbar_init(&q_empty[x], 1);
+      mbar_init(&item_full[x], 1);
+      mbar_init(&item_empty[x], kPtReaders);
+    }
+    mbar_init(tail, 1);
+    mbar_init(fin, 2);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kPtWarpTma) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto fail = [&]() {
+    set_error(g.err, kDevErrTimeout);
+    *abort_flag = 1;
+  };
+  // whole-warp wait
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (*abort_flag || !__all_sync(0xffffffffu, mbar_wait_sleep(bar, parity))) {
+      fail();
+      return false;
+    }
+    return true;
+  };
+  // the warp's next item; false at the end
+  auto next_item = [&](uint32_t k, PtItem& it) -> bool {
+    if (!wait_warp(&item_full[k & 1], (k >> 1) & 1)) return false;
+    it = items[k & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+    return it.valid != 0;
+  };
+
+  if (warp == kPtWarpSched) {
+    // ------------------------------------------------------------ work items
+    uint32_t k = 0;
+    bool ok = true;
+    auto emit = [&](const PtItem& it) -> bool {
+      if (!wait_warp(&item_empty[k & 1], ((k >> 1) & 1) ^ 1)) return ok = false;
+      if (lane == 0) {
+        items[k & 1] = it;
+        mbar_arrive(&item_full[k & 1]);
+      }
+      ++k;
+      __syncwarp();
+      return true;
+    };
+    pt_schedule(a, lane, emit);
+    if (ok) emit(PtItem{});
+  } else if (warp == kPtWarpTma) {
+    // ------------------------------------------------------------ K / V loads
+    const int box = 1 << a.box_shift, boxes = kPtCols >> a.box_shift;
+    int issued[C::kStages];
+    for (int s = 0; s < C::kStages; ++s) issued[s] = -1;
+    uint32_t seq = 0, tails = 0;
+    bool ok = true;
+    PtItem it;
+    for (uint32_t k = 0; ok && next_item(k, it); ++k) {
+      const int nt = max(pt_mine(it, g.G, 0), pt_mine(it, g.G, 1));
+      // lane l's page and first token in it, of box l of column tile t
+      auto page_of = [&](int t) -> int {
+        if (!g.table) return 0;
+        const int col = t * kPtCols + lane * box;
+        if (lane >= boxes || col >= it.L) return g.n_pages;  // outside the tensor: zeros
+        const int page = g.table[(size_t)it.b * g.max_blocks + (col >> g.shift)];
+        if (page < 0 || page >= g.n_pages) {
+          set_error(g.err, FLASHLOOP_DEVERR_INDEX);
+          return g.n_pages;
+        }
+        return page;
+      };
+      int page = nt > 0 ? page_of(it.t0) : 0;
+      for (int i = 0; i < nt && ok; ++i) {
+        const int t = it.t0 + i;
+        const int next = i + 1 < nt ? page_of(t + 1) : 0;
+        const int col = t * kPtCols + lane * box;
+        const int y = g.table ? (col & ((1 << g.shift) - 1)) : it.q0 + col;
+        const int live = it.L - t * kPtCols;  // tokens of the tile before the request's end
+        for (int kv = 0; kv < 2; ++kv, ++seq) {
+          const int slot = seq % C::kStages;
+          const uint32_t ph = (seq / C::kStages) & 1;
+          if (!wait_warp(&kv_empty[slot], ph ^ 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = ring + slot * C::kSlotBytes;
+          const bool clear = kv == 1 && live < kPtCols;
+          uint64_t* bar = clear ? tail : &kv_full[slot];
+          if (lane == 0) mbar_arrive_expect_tx(bar, C::kSlotBytes);
+          __syncwarp();
+          if (lane < boxes) {
+#pragma unroll
+            for (int c = 0; c < DH / 64; ++c)
+              tma_load_4d(st + c * C::kChunk + lane * box * 128, kv ? &tm_v : &tm_k, c * 64, y, it.h, page, bar);
+          }
+          if (clear) {
+            if (!wait_warp(tail, tails & 1)) {
+              ok = false;
+              break;
+            }
+            ++tails;
+            for (int j = lane; j < (kPtCols - live) * 8; j += 32) {
+#pragma unroll
+              for (int c = 0; c < DH / 64; ++c)
+                *reinterpret_cast<uint4*>(st + c * C::kChunk + (live + (j >> 3)) * 128 + (j & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&kv_full[slot]);
+          }
+          issued[slot] = clear ? -1 : (int)ph;  // a cleared one has landed
+        }
+        page = next;
+      }
+    }
+    // never leave with a copy in flight: wait (bounded) for the last load of every slot
+    for (int s = 0; s < C::kStages; ++s)
+      if (issued[s] >= 0) (void)mbar_wait(&kv_full[s], (uint32_t)issued[s]);
+    __syncwarp();
+  } else if (warp == kPtWarpMma || warp == kPtWarpMma + 1) {
+    // ------------------------------------------------------------ MMA issue, one thread per tile
+    if (lane == 0) {
+      const int x = warp - kPtWarpMma;
+      uint32_t seq = 0, u = 0;  // slots so far, column tiles of this tile so far
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        if (*abort_flag || !mbar_wait_sleep(bar, parity)) {
+          fail();
+          ok = false;
+          return false;
+        }
+        tc_fence_after();
+        return true;
+      };
+      auto slot_of = [&](uint32_t s) { return (int)(s % C::kStages); };
+      auto par_of = [&](uint32_t s) { return (s / C::kStages) & 1u; };
+      const uint32_t q = smem_u32(smem + x * C::kQBytes);
+      const uint32_t scol = tmem + kColS + 128u * x;
+      auto issue_s = [&](int slot) {
+        const uint32_t kt = smem_u32(ring + slot * C::kSlotBytes);
+#pragma unroll
+        for (int ks = 0; ks < DH / 16; ++ks)
+          umma_f16(scol, sw128_kmajor_desc(q + (ks >> 2) * C::kQChunk + (ks & 3) * 32),
+                   sw128_kmajor_desc(kt + (ks >> 2) * C::kChunk + (ks & 3) * 32), kIdescS, ks > 0);
+      };
+      auto issue_pv = [&](int slot, int hf, bool acc) {
+        const uint32_t v = smem_u32(ring + slot * C::kSlotBytes) + hf * 64 * 128;
+        const uint32_t d = tmem + (uint32_t)(x * DH), pcol = scol + 64u * hf;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          umma_f16_ts(d, pcol + ks * 8, sw128_mnmajor_desc(v + ks * 2048, C::kChunk), kIdescPV,
+                      (acc || ks > 0) ? 1u : 0u);
+      };
+      // a slot this tile does not read: released once its load has landed
+      auto skip = [&](uint32_t s) -> bool {
+        if (!wait(&kv_full[slot_of(s)], par_of(s))) return false;
+        mbar_arrive(&kv_empty[slot_of(s)]);
+        return true;
+      };
+      for (uint32_t k = 0; ok; ++k) {
+        if (!wait(&item_full[k & 1], (k >> 1) & 1)) break;
+        const PtItem it = items[k & 1];
+        mbar_arrive(&item_empty[k & 1]);
+        if (!it.valid) break;
+        const int mine[2] = {pt_mine(it, g.G, 0), pt_mine(it, g.G, 1)};
+        const int my = mine[x], nt = max(mine[0], mine[1]);
+        if (!wait(&q_full[x], k & 1)) break;
+        const uint32_t base = seq;
+        if (my > 0) {
+          if (!wait(&kv_full[slot_of(base)], par_of(base))) break;
+          issue_s(slot_of(base));
+          umma_commit(&s_full[x]);
+          if (my == 1) umma_commit(&q_empty[x]);
+          umma_commit(&kv_empty[slot_of(base)]);
+        } else {
+          umma_commit(&q_empty[x]);
+          if (nt > 0 && !skip(base)) break;
+        }
+        for (int t = 0; t < nt && ok; ++t) {
+          const uint32_t vs = base + 2 * t + 1, ks_next = base + 2 * t + 2;
+          if (t >= my) {
+            if (!skip(vs)) break;
+            if (t + 1 < nt && !skip(ks_next)) break;
+            continue;
+          }
+          if (!wait(&kv_full[slot_of(vs)], par_of(vs))) break;
+          if (t == 0 && k > 0 && !wait(&n_free[x], (k - 1) & 1)) break;
+          for (int hf = 0; hf < 2; ++hf) {
+            if (!wait(&p_full[2 * x + hf], u & 1)) break;
+            issue_pv(slot_of(vs), hf, t > 0 || hf > 0);
+            umma_commit(&pv_done[x]);
+          }
+          if (!ok) break;
+          ++u;
+          if (t == my - 1) umma_commit(&acc_full[x]);
+          umma_commit(&kv_empty[slot_of(vs)]);
+          if (t + 1 < my) {
+            if (!wait(&kv_full[slot_of(ks_next)], par_of(ks_next))) break;
+            issue_s(slot_of(ks_next));
+            umma_commit(&s_full[x]);
+            if (t + 1 == my - 1) umma_commit(&q_empty[x]);
+            umma_commit(&kv_empty[slot_of(ks_next)]);
+          } else if (t + 1 < nt) {
+            if (!skip(ks_next)) break;
+          }
+        }
+        if (!ok) break;
+        if (my == 0) {
+          if (k > 0 && !wait(&n_free[x], (k - 1) & 1)) break;
+          umma_commit(&acc_full[x]);
+        }
+        seq = base + 2 * nt;
+      }
+      // every MMA issued has completed before TMEM is released
+      umma_commit(fin);
+      (void)mbar_wait(fin, 0);
+    }
+  } else if (warp >= kPtWarpQ) {
+    // ------------------------------------------------------------ queries
+    const int tid = threadIdx.x - kPtWarpQ * 32;
+    constexpr int kPieces = DH / 8;
+    bool ok = true;
+    PtItem it;
+    for (uint32_t k = 0; ok && next_item(k, it); ++k) {
+      const int rows = it.n * g.G;
+      for (int x = 0; x < 2 && ok; ++x) {
+        if (k > 0 && !wait_warp(&q_empty[x], (k - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        uint8_t* dst = smem + x * C::kQBytes;
+#pragma unroll 4
+        for (int i = tid; i < kPtRows * kPieces; i += 128) {
+          const int row = i / kPieces, c = i % kPieces;
+          const int r = it.r0 + x * kPtRows + row;
+          const int tok = r / g.G;
+          const uint16_t* src = g.q.p;
+          if (r < rows) src += (it.q0 + tok) * g.q.st + (long long)(it.h * g.G + r - tok * g.G) * g.q.sh + c * 8;
+          cp_async16(dst + (c >> 3) * C::kQChunk + row * 128 + (((c & 7) ^ (row & 7)) << 4), src, r < rows ? 16 : 0);
+        }
+        cp_async_wait_all();
+        fence_proxy_async_smem();
+        mbar_arrive(&q_full[x]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ rows
+    const int x = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t sbase = tmem + lane_base + kColS + 128u * x;
+    const uint32_t nbase = tmem + lane_base + (uint32_t)(x * DH);
+    const uint64_t scale2 = f2_pack(g.scale_log2, g.scale_log2);
+    uint32_t u = 0;  // column tiles of this tile so far
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      if (!wait_warp(bar, parity)) {
+        ok = false;
+        return false;
+      }
+      tc_fence_after();
+      return true;
+    };
+    PtItem it;
+    for (uint32_t k = 0; ok && next_item(k, it); ++k) {
+      const int my = pt_mine(it, g.G, x);
+      const int r = it.r0 + x * kPtRows + row;
+      const bool live = r < it.n * g.G;
+      const int tok = r / g.G, hq = it.h * g.G + r - tok * g.G;
+      // columns that the row sees; a row behind the last one computes on zero queries and is not written
+      const int seen = live ? max(0, it.L - it.n + tok + 1) : 0x7fffffff;
+      float m_ref = -INFINITY, z = 0.f;
+      for (int t = 0; t < my && ok; ++t, ++u) {
+        if (!wait(&s_full[x], u & 1)) break;
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          const int nvalid = min(max(seen - ((it.t0 + t) * kPtCols + 64 * hf), 0), 64);
+          const uint32_t shalf = sbase + 64u * hf;
+          uint32_t s[64];
+          {
+            uint32_t (&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[0]);
+            uint32_t (&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[32]);
+            tmem_ld32(shalf, s0);
+            tmem_ld32(shalf + 32, s1);
+            tmem_wait_ld();
+          }
+          const bool masked = __any_sync(0xffffffffu, nvalid < 64);
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (e >= nvalid) s[e] = 0xff800000u;  // -inf
+          }
+          const float mx = max64(s) * g.scale_log2;
+          const bool need = mx > m_ref + kPtRescale;
+          if (__any_sync(0xffffffffu, need)) {
+            // raise the reference: z and the numerator so far scale by 2^(m_ref - mx), the
+            // numerator once the previous half's P.V (the last one issued) has completed
+            const float f = need ? ex2(m_ref - mx) : 1.f;
+            if (t > 0 || hf > 0) {
+              if (!wait(&pv_done[x], (2 * u + hf - 1) & 1)) break;
+#pragma unroll 1
+              for (int cc = 0; cc < DH; cc += 16) {
+                uint32_t w[16];
+                tmem_ld16(nbase + cc, w);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+                tmem_st16(nbase + cc, w);
+              }
+            }
+            z *= f;
+            if (need) m_ref = mx;
+          }
+          const float mr = m_ref == -INFINITY ? 0.f : m_ref;
+          const uint64_t neg = f2_pack(-mr, -mr);
+          uint64_t za[2] = {0ull, 0ull};
+          uint32_t pk[32];
+          auto exps = [&](auto poly) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              uint64_t v = f2_fma(f2_pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), scale2, neg);
+              float p0, p1;
+              if (decltype(poly)::value && (e & 3) == 3) {
+                v = exp2_poly2(v);
+                f2_unpack(v, p0, p1);
+              } else {
+                f2_unpack(v, p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                v = f2_pack(p0, p1);
+              }
+              za[e & 1] = f2_add(za[e & 1], v);
+              pk[e] = pg_pack2<BF>(p0, p1);
+            }
+          };
+          // masked halves take ex2 alone: it gives exactly 0 for -inf
+          if (masked) exps(std::false_type{});
+          else exps(std::true_type{});
+          tmem_st32(shalf, pk);
+          float z0, z1, z2, z3;
+          f2_unpack(za[0], z0, z1);
+          f2_unpack(za[1], z2, z3);
+          z += (z0 + z1) + (z2 + z3);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&p_full[2 * x + hf]);
+        }
+      }
+      if (!ok || !wait(&acc_full[x], k & 1)) break;
+      // write-back; a numerator is read once for all rows of the warp, whether live or not
+      uint16_t* od = g.o.p + (live ? (it.q0 + tok) * g.o.st + (long long)hq * g.o.sh : 0);
+      auto put = [&](int cc, const float (&v)[32], float inv) {
+        if (!live) return;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          *reinterpret_cast<uint4*>(od + cc + 8 * w) =
+              make_uint4(pg_pack2<BF>(v[8 * w] * inv, v[8 * w + 1] * inv), pg_pack2<BF>(v[8 * w + 2] * inv, v[8 * w + 3] * inv),
+                         pg_pack2<BF>(v[8 * w + 4] * inv, v[8 * w + 5] * inv), pg_pack2<BF>(v[8 * w + 6] * inv, v[8 * w + 7] * inv));
+      };
+      auto put_lse = [&](float m, float zz) {
+        if (live && g.lse)
+          g.lse[(size_t)hq * g.max_tokens + it.q0 + tok] = zz == 0.f ? -INFINITY : (m + log2f(zz)) * kPgLn2;
+      };
+      const size_t prow = (size_t)it.slot * kPtPair + x * kPtRows + row;
+      const float inv = z == 0.f ? 0.f : 1.f / z;
+#pragma unroll 1
+      for (int cc = 0; cc < DH; cc += 32) {
+        uint32_t w[32];
+        float v[32];
+        if (my > 0) {
+          tmem_ld32(nbase + cc, w);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = my > 0 ? __uint_as_float(w[e]) : 0.f;
+        if (it.parts == 1) {
+          put(cc, v, inv);
+        } else if (live && my > 0) {
+          float4* d = reinterpret_cast<float4*>(a.part_n + prow * DH + cc);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) __stcg(d + e, make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&n_free[x]);
+      if (it.parts == 1) {
+        put_lse(m_ref, z);
+        continue;
+      }
+      // a part: the block that finishes last joins them, in their order
+      __stcg(a.part_mz + prow, make_float2(my > 0 ? m_ref : -INFINITY, my > 0 ? z : 0.f));
+      __threadfence();
+      named_bar_sync(1 + x, kPtRows);
+      if (row == 0) {
+        const uint32_t done = atomicAdd(&a.tickets[it.slot0 * 2 + x], 1u);
+        __threadfence();
+        last_flag[x] = done == (uint32_t)(it.parts - 1);
+      }
+      named_bar_sync(1 + x, kPtRows);
+      if (last_flag[x]) {
+        __threadfence();
+        const size_t row0 = (size_t)it.slot0 * kPtPair + x * kPtRows + row;
+        // part i > 0 lies in its block's first slot
+        const size_t block0 = (size_t)(it.slot0 >> 1);
+        auto prow_of = [&](int i) { return i == 0 ? row0 : ((block0 + i) * 2) * kPtPair + x * kPtRows + row; };
+        float mm = -INFINITY, zz = 0.f;
+        for (int i = 0; i < it.parts; ++i) mm = fmaxf(mm, __ldcg(a.part_mz + prow_of(i)).x);
+        for (int i = 0; i < it.parts; ++i) {
+          const float2 mz = __ldcg(a.part_mz + prow_of(i));
+          if (mz.x != -INFINITY || mz.y != 0.f) zz += mz.y * ex2(mz.x - mm);
+        }
+        const float minv = zz == 0.f ? 0.f : 1.f / zz;
+#pragma unroll 1
+        for (int cc = 0; cc < DH; cc += 32) {
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0.f;
+          for (int i = 0; i < it.parts; ++i) {
+            const float2 mz = __ldcg(a.part_mz + prow_of(i));
+            if (!live || (mz.x == -INFINITY && mz.y == 0.f)) continue;
+            const float f = ex2(mz.x - mm);
+            const float4* d = reinterpret_cast<const float4*>(a.part_n + prow_of(i) * DH + cc);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 n4 = __ldcg(d + e);
+              v[4 * e] += f * n4.x;
+              v[4 * e + 1] += f * n4.y;
+              v[4 * e + 2] += f * n4.z;
+              v[4 * e + 3] += f * n4.w;
+            }
+          }
+          put(cc, v, minv);
+        }
+        put_lse(mm, zz);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kPtWarpTma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+int at_sm_count();
+
+// A 16-bit tensor [d3, d2, d1, DH] (strides in elements) whose boxes are `rows`
+// tokens of 64 elements, 128-byte swizzle; what lies outside reads as zero.
+static int pt_tmap(CUtensorMap* map, const PgPages& t, int bf16, uint64_t dh, uint64_t tokens, uint64_t heads,
+                   uint64_t pages, uint32_t rows) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    return nullptr;
+  }();
+  if (fn == nullptr) return FLASHLOOP_ERR_CUDA;
+  // a dimension of one has no stride of its own
+  const long long sh = heads > 1 ? t.sh : (long long)dh, sp = pages > 1 ? t.sp : (long long)dh;
+  const long long st = tokens > 1 ? t.st : (long long)dh;
+  cuuint64_t dims[4] = {dh, tokens, heads, pages};
+  cuuint64_t strides[3] = {(cuuint64_t)st * 2, (cuuint64_t)sh * 2, (cuuint64_t)sp * 2};
+  cuuint32_t box[4] = {64, rows, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                        const_cast<uint16_t*>(t.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FLASHLOOP_OK : FLASHLOOP_ERR_CUDA;
+}
+
+int launch_pg_tile(const PgArgs& g, int dh, int bf16, int few, const PgScratch& ws, cudaStream_t stream) {
+  PtArgs a{};
+  a.g = g;
+  a.few = few;
+  a.box_shift = g.table && g.shift < 7 ? g.shift : 7;
+  a.tickets = ws.tile_tickets;
+  a.part_mz = ws.tile_mz;
+  a.part_n = ws.tile_n;
+  const uint64_t tokens = g.table ? 1ull << g.shift : (uint64_t)g.max_tokens;
+  const uint64_t pages = g.table ? (uint64_t)g.n_pages : 1;
+  const uint32_t rows = 1u << a.box_shift;
+  CUtensorMap tk, tv;
+  int rc = pt_tmap(&tk, g.k, bf16, dh, tokens, g.Hk, pages, rows);
+  if (rc == FLASHLOOP_OK) rc = pt_tmap(&tv, g.v, bf16, dh, tokens, g.Hk, pages, rows);
+  if (rc != FLASHLOOP_OK) return rc;
+  int grid = at_sm_count();
+  if (grid > kPgSms) grid = kPgSms;
+  if (!a.tickets) {
+    const long long items = (long long)g.Hk * (((long long)g.max_tokens * g.G + kPtPair - 1) / kPtPair + g.B);
+    if (grid > items) grid = (int)items;
+  }
+  auto go = [&](auto kernel, int smem) -> int {
+    FL_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    kernel<<<grid, kPtThreads, smem, stream>>>(tk, tv, a);
+    return launch_status();
+  };
+  if (dh == 128) {
+    if (bf16) return go(pg_tile_kernel<128, 1>, PtCfg<128>::kSmem);
+    return go(pg_tile_kernel<128, 0>, PtCfg<128>::kSmem);
+  }
+  if (bf16) return go(pg_tile_kernel<64, 1>, PtCfg<64>::kSmem);
+  return go(pg_tile_kernel<64, 0>, PtCfg<64>::kSmem);
+}
+
+}  // namespace fl

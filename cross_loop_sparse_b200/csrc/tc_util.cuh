@@ -266,3 +266,85 @@ __device__ __forceinline__ void tma_gather4(void* dst, const void* tmap, int x, 
 }
 
 }  // namespace fl
+
+namespace fl {
+
+// 4-D TMA tile load (coordinates innermost first).
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n"
+      ::"r"(smem_u32(dst)), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Shared-memory descriptor of an operand stored with K as the row (MN-major),
+// 128-byte swizzle: a row holds 64 consecutive MN elements, 8 rows are an atom
+// of 1024 bytes, the next 8 rows follow it (stride offset 1024 B), and the next
+// 64 MN elements start `mn_stride` bytes on (leading offset).  `saddr` advances
+// by 2048 B per K=16 step.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t mn_stride) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((mn_stride >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+// Instruction-descriptor bit of an MN-major B operand.
+constexpr uint32_t kIdescBMnMajor = 1u << 16;
+
+// Packed float32 pairs in a 64-bit register.
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 2^x of a pair on the FMA units, for -126 <= x <= 126 (smaller x counts as
+// -126): x = k + r with k the nearest integer (added and taken away with the
+// constant 1.5 * 2^23, whose low mantissa bits then hold k), 2^r on [-1/2, 1/2]
+// by a degree-5 polynomial fitted to the smallest relative error (2.2e-7 with
+// the roundings), and k added to the exponent field.  NaN gives a value that
+// is not finite or near the largest float32.
+__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  asm("max.NaN.f32 %0, %0, %1;\n" : "+f"(a) : "f"(-126.f));
+  asm("max.NaN.f32 %0, %0, %1;\n" : "+f"(b) : "f"(-126.f));
+  const uint64_t v = f2_pack(a, b), magic = f2_pack(12582912.f, 12582912.f);
+  const uint64_t t = f2_add(v, magic);
+  const uint64_t r = f2_sub(v, f2_sub(t, magic));
+  uint64_t p = f2_pack(0.001327647129073739f, 0.001327647129073739f);
+  p = f2_fma(p, r, f2_pack(0.009675540961325169f, 0.009675540961325169f));
+  p = f2_fma(p, r, f2_pack(0.05550713092088699f, 0.05550713092088699f));
+  p = f2_fma(p, r, f2_pack(0.24022120237350464f, 0.24022120237350464f));
+  p = f2_fma(p, r, f2_pack(0.6931469440460205f, 0.6931469440460205f));
+  p = f2_fma(p, r, f2_pack(1.0000001192092896f, 1.0000001192092896f));
+  float p0, p1, t0, t1;
+  f2_unpack(p, p0, p1);
+  f2_unpack(t, t0, t1);
+  p0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+  p1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+  return f2_pack(p0, p1);
+}
+
+}  // namespace fl

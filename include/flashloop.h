@@ -517,7 +517,7 @@ typedef struct flashloop_paged_params {
   int32_t n_pages;    /* pages of the pool; n_pages * page_size < 2^31 */
   int32_t max_blocks; /* columns of block_table; max_blocks * page_size < 2^31 */
   int32_t dtype;      /* of q, the cache and o: FLASHLOOP_DTYPE_BF16 or _FP16 */
-  float scale;        /* of q.k, usually 1/sqrt(head_dim) */
+  float scale;        /* of q.k, > 0, usually 1/sqrt(head_dim) */
 } flashloop_paged_params;
 
 /* Rows [max_tokens, heads, head_dim]: strides in elements, head_dim contiguous.
