@@ -108,4 +108,14 @@ __device__ __forceinline__ float max64(const uint32_t (&s)[64]) {
   return max3f(max3f(b[0], b[1], b[2]), max3f(b[3], b[4], b[5]), fmaxf(b[6], b[7]));
 }
 
+// Largest of 32 values (a tree of three-input maxima).
+__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
+  float a[11];
+#pragma unroll
+  for (int i = 0; i < 10; ++i)
+    a[i] = max3f(__uint_as_float(s[3 * i]), __uint_as_float(s[3 * i + 1]), __uint_as_float(s[3 * i + 2]));
+  a[10] = fmaxf(__uint_as_float(s[30]), __uint_as_float(s[31]));
+  return max3f(max3f(a[0], a[1], a[2]), max3f(a[3], a[4], a[5]), max3f(max3f(a[6], a[7], a[8]), a[9], a[10]));
+}
+
 }  // namespace fl

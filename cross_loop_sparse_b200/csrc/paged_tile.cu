@@ -20,25 +20,34 @@
 // handed on, since 0 * NaN would reach the rows.
 // TMEM (512 columns): N_A, N_B, then the tiles' 128-column scores; the P of a
 // 64-column half is written over the half's first 32 score columns and feeds
-// that half's P.V from TMEM.  The score MMA is 128 wide (two 64-wide ones read
-// the queries twice and are bound by shared memory).
+// that half's P.V from TMEM.  The next tile's scores of a half are issued right
+// behind that P.V, so that they are there when the rows have done the other
+// half.  A score MMA is 64 wide for this: it takes 48 cycles a k step where 32
+// would do (it reads the queries for half as many columns, and shared memory
+// gives 128 bytes a clock), but 128-wide ones, at their full rate, leave the rows
+// waiting for a whole P.V and score MMA a tile: 4.1 ms against 3.5 ms for a
+// prompt of 32768 tokens x 16 heads.
 //
 // Roles (16 warps): 0-3 / 4-7 rows of tile A / B, one thread a row; 8-11
 // queries of the next item; 12 TMEM and K / V loads (lane = page of a tile);
-// 13 / 14 MMA issue of tile A / B; 15 work items.  While one tile's rows take
-// their exponentials the other tile's MMAs run.  A quarter of the exponentials
-// of unmasked halves is taken by polynomial on the FMA units: MUFU's 16 a
-// clock would need as long for a tile as its MMAs do.
+// 13 / 14 MMA issue of tile A / B; 15 work items.
 //
-// Work: without scratch (prompts) an item is a whole row pair, long ones first
-// within a head.  With scratch (paged) the column tiles of all items are one
+// What bounds it, a pair of 128-column tiles: the MMAs take 2560 cycles (1536
+// scores, 1024 P.V), the exponentials 2300 (MUFU gives 16 a clock; a row thread's
+// other instructions fit beside them), and a pair takes 3450 as they meet.
+// Exponentials by polynomial on the FMA units were no gain at any share: two
+// warps a scheduler cannot keep both units fed (1101 cycles a half with a quarter
+// of them against 1166 without, alone, and a slower kernel).
+//
+// Work: without scratch (prompts) an item is a whole row pair, dealt to and fro
+// from a list that begins with the longest.  With scratch (paged) the column tiles of all items are one
 // line that is cut into equal lengths, one a block, so that few rows over a
 // long cache still use every SM; an item cut by a border is joined by the
 // block that finishes last (float32 N, m, z in scratch, in the order of its
 // parts, so that results do not depend on timing).
 //
-// Every wait is bounded; one that gives up sets FLASHLOOP_DEVERR_TIMEOUT and
-// the block unwinds.
+// Every wait is bounded; one that gives up sets FLASHLOOP_DEVERR_TIMEOUT, and the
+// block unwinds.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -55,6 +64,7 @@ constexpr int kPtCols = 128;
 constexpr int kPtThreads = 512;
 constexpr int kPtWarpQ = 8, kPtWarpTma = 12, kPtWarpMma = 13, kPtWarpSched = 15;
 constexpr float kPtRescale = 8.f;
+constexpr int kPtRegsRows = 192, kPtRegsRest = 64;  // of the 65536 registers: 256 threads of each
 constexpr int kPtReaders = 15;   // arrivals that free a work item's slot: 8 + 4 + 1 + 2 warps
 constexpr int kPtMinUnits = 4;   // column tiles a block takes at least when the line is cut
 
@@ -100,6 +110,14 @@ __device__ __forceinline__ int pt_units(int n, int L, int G, int p) {
   return max(1, pt_tiles(n, L, G, (p + 1) * kPtPair));
 }
 
+// First of np pairs with at least `units` column tiles (they grow with the pair); np if none.
+__device__ __forceinline__ int pt_first_pair(int n, int L, int G, int np, int units) {
+  const long long x = (long long)(units - 1) * kPtCols - (L - n);  // its last row's position, at least
+  if (units <= 1 || x <= 0) return 0;
+  if (x > n - 1) return np;
+  return (int)min((long long)np - 1, (x * G + kPtPair) / kPtPair - 1);
+}
+
 // Warp 15: cuts the work into items.  `emit` returns false when the block ends.
 template <typename Emit>
 __device__ __forceinline__ void pt_schedule(const PtArgs& a, int lane, Emit emit) {
@@ -115,37 +133,43 @@ __device__ __forceinline__ void pt_schedule(const PtArgs& a, int lane, Emit emit
     np = pt_pairs(a, s.n);
   };
   if (a.tickets == nullptr) {
-    // whole items, block i takes items i, i + grid, ...
-    long long item = blockIdx.x, base = 0;
-    for (int b0 = 0; b0 < g.B; b0 += 32) {
-      chunk(b0);
-      const long long mine = (long long)np * g.Hk;
-      long long end = mine;
+    // whole items, dealt out to and fro (block c takes items c, 2 grid - 1 - c, 2 grid + c, ...) from
+    // a list that begins with the longest: those of 2^c column tiles and more, c falling, and
+    // within a class and request the last rows first
+    long long item = blockIdx.x, round = 0, base = 0;
+    int loaded = -1;
+    for (int cls = 31 - __clz(max(1, (g.max_new + kPtCols - 1) / kPtCols)); cls >= 0; --cls) {
+      for (int b0 = 0; b0 < g.B; b0 += 32) {
+        if (loaded != b0) chunk(b0);
+        loaded = b0;
+        const int p0 = pt_first_pair(s.n, s.L, G, np, 1 << cls), p1 = pt_first_pair(s.n, s.L, G, np, 2 << cls);
+        const long long mine = (long long)(p1 - p0) * g.Hk;
+        long long end = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(kAll, end, o);
-        if (lane >= o) end += y;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(kAll, end, o);
+          if (lane >= o) end += y;
+        }
+        const long long total = __shfl_sync(kAll, end, 31);
+        while (item < base + total) {
+          const int src = __ffs(__ballot_sync(kAll, base + end > item)) - 1;
+          const int idx = (int)(item - base - __shfl_sync(kAll, end - mine, src));
+          PtItem it{};
+          it.valid = 1;
+          it.b = b0 + src;
+          it.h = idx % g.Hk;
+          it.q0 = __shfl_sync(kAll, s.q0, src);
+          it.n = __shfl_sync(kAll, s.n, src);
+          it.L = __shfl_sync(kAll, s.L, src);
+          it.r0 = (__shfl_sync(kAll, p1, src) - 1 - idx / g.Hk) * kPtPair;
+          it.t1 = pt_tiles(it.n, it.L, G, it.r0 + kPtPair);
+          it.parts = 1;
+          if (!emit(it)) return;
+          ++round;
+          item = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        }
+        base += total;
       }
-      const long long total = __shfl_sync(kAll, end, 31);
-      while (item < base + total) {
-        const int src = __ffs(__ballot_sync(kAll, base + end > item)) - 1;
-        const int n_p = __shfl_sync(kAll, np, src);
-        const long long idx = item - base - __shfl_sync(kAll, end - mine, src);
-        PtItem it{};
-        it.valid = 1;
-        it.b = b0 + src;
-        it.h = (int)(idx / n_p);
-        it.q0 = __shfl_sync(kAll, s.q0, src);
-        it.n = __shfl_sync(kAll, s.n, src);
-        it.L = __shfl_sync(kAll, s.L, src);
-        const int p = n_p - 1 - (int)(idx % n_p);  // long rows first
-        it.r0 = p * kPtPair;
-        it.t1 = pt_tiles(it.n, it.L, G, it.r0 + kPtPair);
-        it.parts = 1;
-        if (!emit(it)) return;
-        item += gridDim.x;
-      }
-      base += total;
     }
     return;
   }
@@ -245,11 +269,30 @@ __device__ __forceinline__ int pt_mine(const PtItem& it, int G, int x) {
   return max(0, min(it.t1, pt_tiles(it.n, it.L, G, first + kPtRows)) - it.t0);
 }
 
+// Registers move from the warpgroups of the other roles to the rows', which
+// hold a whole row of scores: the shares sum to what the block launched with.
+template <int N>
+__device__ __forceinline__ void pt_regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void pt_regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+static_assert(256 * kPtRegsRows + 256 * kPtRegsRest <= kPtThreads * 128, "registers of the block");
+
+// Columns from nvalid on count as -inf.
+__device__ __forceinline__ void pt_mask(uint32_t (&s)[32], int nvalid) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (e >= nvalid) s[e] = 0xff800000u;
+}
+
 template <int DH, int BF>
 __global__ void __launch_bounds__(kPtThreads, 1)
 pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, PtArgs a) {
   using C = PtCfg<DH>;
-  constexpr uint32_t kIdescS = f16_idesc(128, 128, BF);
+  constexpr uint32_t kIdescS = f16_idesc(128, 64, BF);
   constexpr uint32_t kIdescPV = f16_idesc(128, DH, BF) | kIdescBMnMajor;
   constexpr uint32_t kColS = 256;  // tile x: scores at 256 + 128 x, numerator at x * DH
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -257,11 +300,11 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* kv_full = bars;                  // [stages] a slot's bytes landed
   uint64_t* kv_empty = bars + C::kStages;    // [stages] both issuers done with the slot
-  uint64_t* s_full = bars + 2 * C::kStages;  // [x] scores of a column tile in TMEM
-  uint64_t* p_full = s_full + 2;             // [x * 2 + half] P of a half written (128 threads)
-  uint64_t* pv_done = p_full + 4;            // [x] a half's P.V completed (two a column tile)
-  uint64_t* acc_full = pv_done + 2;          // [x] the item's last P.V completed
-  uint64_t* n_free = acc_full + 2;           // [x] the numerator has been read (128 threads)
+  uint64_t* s_full = bars + 2 * C::kStages;  // [x * 2 + half] scores of a half column tile in TMEM
+  uint64_t* p_full = s_full + 4;             // [x * 2 + half] P of a half written (4 warps)
+  uint64_t* pv0_done = p_full + 4;           // [x] the item's last first-half P.V completed
+  uint64_t* acc_full = pv0_done + 2;         // [x] the item's last P.V completed
+  uint64_t* n_free = acc_full + 2;           // [x] the numerator has been read (4 warps)
   uint64_t* q_full = n_free + 2;             // [x] queries stored (128 threads)
   uint64_t* q_empty = q_full + 2;            // [x] the item's score MMAs completed
   uint64_t* item_full = q_empty + 2;         // [2]
@@ -269,7 +312,6 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   uint64_t* tail = item_empty + 2;           // [1] bytes of a V tile whose last rows are cleared
   uint64_t* fin = tail + 1;                  // [1] every MMA of both issuers completed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* last_flag = reinterpret_cast<int*>(tmem_slot + 2);  // [x]
   PtItem* items = reinterpret_cast<PtItem*>(tmem_slot + 4);  // [2]
   static_assert((2 * C::kStages + 24) * 8 + 16 + 2 * sizeof(PtItem) <= 512, "barriers");
@@ -282,12 +324,14 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 2);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], kPtRows);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], kPtRows / 32);
+    }
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&s_full[x], 1);
-      mbar_init(&pv_done[x], 1);
+      mbar_init(&pv0_done[x], 1);
       mbar_init(&acc_full[x], 1);
-      mbar_init(&n_free[x], kPtRows);
+      mbar_init(&n_free[x], kPtRows / 32);
       mbar_init(&q_full[x], kPtRows);
       mbar_init(&q_empty[x], 1);
       mbar_init(&item_full[x], 1);
@@ -295,7 +339,6 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     }
     mbar_init(tail, 1);
     mbar_init(fin, 2);
-    *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kPtWarpTma) {
@@ -307,13 +350,11 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  auto fail = [&]() {
-    set_error(g.err, kDevErrTimeout);
-    *abort_flag = 1;
-  };
+  // a role whose wait gave up stops arriving, so that the others' waits give up in turn
+  auto fail = [&]() { set_error(g.err, kDevErrTimeout); };
   // whole-warp wait
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (*abort_flag || !__all_sync(0xffffffffu, mbar_wait_sleep(bar, parity))) {
+    if (!__all_sync(0xffffffffu, mbar_wait_sleep(bar, parity))) {
       fail();
       return false;
     }
@@ -330,6 +371,7 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 
   if (warp == kPtWarpSched) {
     // ------------------------------------------------------------ work items
+    pt_regs_dec<kPtRegsRest>();
     uint32_t k = 0;
     bool ok = true;
     auto emit = [&](const PtItem& it) -> bool {
@@ -346,9 +388,8 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     if (ok) emit(PtItem{});
   } else if (warp == kPtWarpTma) {
     // ------------------------------------------------------------ K / V loads
+    pt_regs_dec<kPtRegsRest>();
     const int box = 1 << a.box_shift, boxes = kPtCols >> a.box_shift;
-    int issued[C::kStages];
-    for (int s = 0; s < C::kStages; ++s) issued[s] = -1;
     uint32_t seq = 0, tails = 0;
     bool ok = true;
     PtItem it;
@@ -406,23 +447,23 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             __syncwarp();
             if (lane == 0) mbar_arrive(&kv_full[slot]);
           }
-          issued[slot] = clear ? -1 : (int)ph;  // a cleared one has landed
         }
         page = next;
       }
     }
     // never leave with a copy in flight: wait (bounded) for the last load of every slot
-    for (int s = 0; s < C::kStages; ++s)
-      if (issued[s] >= 0) (void)mbar_wait(&kv_full[s], (uint32_t)issued[s]);
+    for (uint32_t i = seq > C::kStages ? seq - C::kStages : 0; i < seq; ++i)
+      (void)mbar_wait(&kv_full[i % C::kStages], (i / C::kStages) & 1);
     __syncwarp();
   } else if (warp == kPtWarpMma || warp == kPtWarpMma + 1) {
     // ------------------------------------------------------------ MMA issue, one thread per tile
+    pt_regs_dec<kPtRegsRest>();
     if (lane == 0) {
       const int x = warp - kPtWarpMma;
       uint32_t seq = 0, u = 0;  // slots so far, column tiles of this tile so far
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        if (*abort_flag || !mbar_wait_sleep(bar, parity)) {
+        if (!mbar_wait_sleep(bar, parity)) {
           fail();
           ok = false;
           return false;
@@ -434,11 +475,11 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       auto par_of = [&](uint32_t s) { return (s / C::kStages) & 1u; };
       const uint32_t q = smem_u32(smem + x * C::kQBytes);
       const uint32_t scol = tmem + kColS + 128u * x;
-      auto issue_s = [&](int slot) {
-        const uint32_t kt = smem_u32(ring + slot * C::kSlotBytes);
+      auto issue_s = [&](int slot, int hf) {
+        const uint32_t kt = smem_u32(ring + slot * C::kSlotBytes) + hf * 64 * 128;
 #pragma unroll
         for (int ks = 0; ks < DH / 16; ++ks)
-          umma_f16(scol, sw128_kmajor_desc(q + (ks >> 2) * C::kQChunk + (ks & 3) * 32),
+          umma_f16(scol + 64u * hf, sw128_kmajor_desc(q + (ks >> 2) * C::kQChunk + (ks & 3) * 32),
                    sw128_kmajor_desc(kt + (ks >> 2) * C::kChunk + (ks & 3) * 32), kIdescS, ks > 0);
       };
       auto issue_pv = [&](int slot, int hf, bool acc) {
@@ -466,42 +507,43 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const uint32_t base = seq;
         if (my > 0) {
           if (!wait(&kv_full[slot_of(base)], par_of(base))) break;
-          issue_s(slot_of(base));
-          umma_commit(&s_full[x]);
+          for (int hf = 0; hf < 2; ++hf) {
+            issue_s(slot_of(base), hf);
+            umma_commit(&s_full[2 * x + hf]);
+          }
           if (my == 1) umma_commit(&q_empty[x]);
           umma_commit(&kv_empty[slot_of(base)]);
+          if (k > 0 && !wait(&n_free[x], (k - 1) & 1)) break;
         } else {
           umma_commit(&q_empty[x]);
           if (nt > 0 && !skip(base)) break;
         }
-        for (int t = 0; t < nt && ok; ++t) {
-          const uint32_t vs = base + 2 * t + 1, ks_next = base + 2 * t + 2;
-          if (t >= my) {
-            if (!skip(vs)) break;
-            if (t + 1 < nt && !skip(ks_next)) break;
-            continue;
-          }
+        // A tile's V and the next tile's K are waited for before its P, and slots are given
+        // back behind the next scores: between a P and those lies MMA issue alone.
+        for (int t = 0; t < my && ok; ++t, ++u) {
+          const uint32_t vs = base + 2 * t + 1, ks = vs + 1;
+          const bool more = t + 1 < my;
           if (!wait(&kv_full[slot_of(vs)], par_of(vs))) break;
-          if (t == 0 && k > 0 && !wait(&n_free[x], (k - 1) & 1)) break;
+          if (more && !wait(&kv_full[slot_of(ks)], par_of(ks))) break;
           for (int hf = 0; hf < 2; ++hf) {
             if (!wait(&p_full[2 * x + hf], u & 1)) break;
             issue_pv(slot_of(vs), hf, t > 0 || hf > 0);
-            umma_commit(&pv_done[x]);
+            if (more) {
+              issue_s(slot_of(ks), hf);
+              umma_commit(&s_full[2 * x + hf]);
+            } else {
+              umma_commit(hf ? &acc_full[x] : &pv0_done[x]);
+            }
           }
           if (!ok) break;
-          ++u;
-          if (t == my - 1) umma_commit(&acc_full[x]);
           umma_commit(&kv_empty[slot_of(vs)]);
-          if (t + 1 < my) {
-            if (!wait(&kv_full[slot_of(ks_next)], par_of(ks_next))) break;
-            issue_s(slot_of(ks_next));
-            umma_commit(&s_full[x]);
-            if (t + 1 == my - 1) umma_commit(&q_empty[x]);
-            umma_commit(&kv_empty[slot_of(ks_next)]);
-          } else if (t + 1 < nt) {
-            if (!skip(ks_next)) break;
+          if (more) {
+            umma_commit(&kv_empty[slot_of(ks)]);
+            if (t + 2 == my) umma_commit(&q_empty[x]);
           }
         }
+        // slots of column tiles that the other tile alone reads
+        for (uint32_t s = base + (my > 0 ? 2 * my : 1); ok && s < base + 2 * nt; ++s) skip(s);
         if (!ok) break;
         if (my == 0) {
           if (k > 0 && !wait(&n_free[x], (k - 1) & 1)) break;
@@ -515,6 +557,7 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     }
   } else if (warp >= kPtWarpQ) {
     // ------------------------------------------------------------ queries
+    pt_regs_dec<kPtRegsRest>();
     const int tid = threadIdx.x - kPtWarpQ * 32;
     constexpr int kPieces = DH / 8;
     bool ok = true;
@@ -543,13 +586,14 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     }
   } else {
     // ------------------------------------------------------------ rows
+    pt_regs_inc<kPtRegsRows>();
     const int x = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const uint32_t sbase = tmem + lane_base + kColS + 128u * x;
     const uint32_t nbase = tmem + lane_base + (uint32_t)(x * DH);
     const uint64_t scale2 = f2_pack(g.scale_log2, g.scale_log2);
-    uint32_t u = 0;  // column tiles of this tile so far
+    uint32_t u = 0, full = 0;  // column tiles of this tile, and items with some, so far
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       if (!wait_warp(bar, parity)) {
@@ -559,43 +603,70 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       tc_fence_after();
       return true;
     };
-    PtItem it;
-    for (uint32_t k = 0; ok && next_item(k, it); ++k) {
+    for (uint32_t k = 0; ok; ++k) {
+      // the item's slot is kept until the write-back has read it: the column loop needs the registers
+      if (!wait(&item_full[k & 1], (k >> 1) & 1)) break;
+      const PtItem& it = items[k & 1];
+      auto release = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+      };
+      if (!it.valid) {
+        release();
+        break;
+      }
       const int my = pt_mine(it, g.G, x);
-      const int r = it.r0 + x * kPtRows + row;
-      const bool live = r < it.n * g.G;
-      const int tok = r / g.G, hq = it.h * g.G + r - tok * g.G;
-      // columns that the row sees; a row behind the last one computes on zero queries and is not written
-      const int seen = live ? max(0, it.L - it.n + tok + 1) : 0x7fffffff;
+      // columns of the item's that the row sees; a row behind the last one computes on zero queries and is not written
+      int seen = 0x7fffffff;
+      {
+        const int r = it.r0 + x * kPtRows + row;
+        if (r < it.n * g.G) seen = it.L - it.n + r / g.G + 1 - it.t0 * kPtCols;
+      }
       float m_ref = -INFINITY, z = 0.f;
       for (int t = 0; t < my && ok; ++t, ++u) {
-        if (!wait(&s_full[x], u & 1)) break;
 #pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
-          const int nvalid = min(max(seen - ((it.t0 + t) * kPtCols + 64 * hf), 0), 64);
-          const uint32_t shalf = sbase + 64u * hf;
-          uint32_t s[64];
-          {
-            uint32_t (&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[0]);
-            uint32_t (&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[32]);
-            tmem_ld32(shalf, s0);
-            tmem_ld32(shalf + 32, s1);
-            tmem_wait_ld();
+          if (!wait(&s_full[2 * x + hf], u & 1)) break;
+          const uint32_t at = sbase + 64u * hf;
+          const int nvalid = seen - t * kPtCols - hf * 64;
+          uint32_t s0[32], s1[32];
+          tmem_ld32(at, s0);
+          tmem_ld32(at + 32, s1);
+          tmem_wait_ld();
+          if (__any_sync(0xffffffffu, nvalid < 64)) {
+            pt_mask(s0, nvalid);
+            pt_mask(s1, nvalid - 32);
           }
-          const bool masked = __any_sync(0xffffffffu, nvalid < 64);
-          if (masked) {
+          // The exponentials are taken on the reference as it is, beside the maximum that says
+          // whether it will do: one score in thousands of tiles says no, and they are taken again.
+          uint32_t pk[32];
+          uint64_t za[2];
+          auto exps = [&]() {
+            const float mr = m_ref == -INFINITY ? 0.f : m_ref;
+            const uint64_t neg = f2_pack(-mr, -mr);
+            za[0] = za[1] = 0ull;
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (e >= nvalid) s[e] = 0xff800000u;  // -inf
-          }
-          const float mx = max64(s) * g.scale_log2;
+            for (int e = 0; e < 32; ++e) {
+              const uint32_t a0 = e < 16 ? s0[(2 * e) & 31] : s1[(2 * e) & 31], a1 = e < 16 ? s0[(2 * e + 1) & 31] : s1[(2 * e + 1) & 31];
+              float p0, p1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(a0), __uint_as_float(a1)), scale2, neg), p0, p1);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              za[e & 1] = f2_add(za[e & 1], f2_pack(p0, p1));
+              pk[e] = pg_pack2<BF>(p0, p1);
+            }
+          };
+          exps();
+          const float mx = fmaxf(max32(s0), max32(s1)) * g.scale_log2;
           const bool need = mx > m_ref + kPtRescale;
           if (__any_sync(0xffffffffu, need)) {
-            // raise the reference: z and the numerator so far scale by 2^(m_ref - mx), the
-            // numerator once the previous half's P.V (the last one issued) has completed
+            // raise it: z and the numerator so far scale by 2^(m_ref - mx) once the last P.V has
+            // completed; the scores that were issued behind it say so
             const float f = need ? ex2(m_ref - mx) : 1.f;
+            uint64_t* behind = hf == 0 ? &s_full[2 * x + 1] : t + 1 < my ? &s_full[2 * x] : &pv0_done[x];
+            const uint32_t phase = hf == 0 ? u : t + 1 < my ? u + 1 : full;
+            if ((t > 0 || hf > 0) && !wait(behind, phase & 1)) break;
             if (t > 0 || hf > 0) {
-              if (!wait(&pv_done[x], (2 * u + hf - 1) & 1)) break;
 #pragma unroll 1
               for (int cc = 0; cc < DH; cc += 16) {
                 uint32_t w[16];
@@ -608,43 +679,24 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             }
             z *= f;
             if (need) m_ref = mx;
+            exps();
           }
-          const float mr = m_ref == -INFINITY ? 0.f : m_ref;
-          const uint64_t neg = f2_pack(-mr, -mr);
-          uint64_t za[2] = {0ull, 0ull};
-          uint32_t pk[32];
-          auto exps = [&](auto poly) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              uint64_t v = f2_fma(f2_pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), scale2, neg);
-              float p0, p1;
-              if (decltype(poly)::value && (e & 3) == 3) {
-                v = exp2_poly2(v);
-                f2_unpack(v, p0, p1);
-              } else {
-                f2_unpack(v, p0, p1);
-                p0 = ex2(p0);
-                p1 = ex2(p1);
-                v = f2_pack(p0, p1);
-              }
-              za[e & 1] = f2_add(za[e & 1], v);
-              pk[e] = pg_pack2<BF>(p0, p1);
-            }
-          };
-          // masked halves take ex2 alone: it gives exactly 0 for -inf
-          if (masked) exps(std::false_type{});
-          else exps(std::true_type{});
-          tmem_st32(shalf, pk);
+          tmem_st32(at, pk);
           float z0, z1, z2, z3;
           f2_unpack(za[0], z0, z1);
           f2_unpack(za[1], z2, z3);
           z += (z0 + z1) + (z2 + z3);
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(&p_full[2 * x + hf]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * x + hf]);
         }
       }
       if (!ok || !wait(&acc_full[x], k & 1)) break;
+      full += my > 0;
+      const int r = it.r0 + x * kPtRows + row;
+      const bool live = r < it.n * g.G;
+      const int tok = r / g.G, hq = it.h * g.G + r - tok * g.G;
       // write-back; a numerator is read once for all rows of the warp, whether live or not
       uint16_t* od = g.o.p + (live ? (it.q0 + tok) * g.o.st + (long long)hq * g.o.sh : 0);
       auto put = [&](int cc, const float (&v)[32], float inv) {
@@ -680,9 +732,11 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
       }
       tc_fence_before();
-      mbar_arrive(&n_free[x]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&n_free[x]);
       if (it.parts == 1) {
         put_lse(m_ref, z);
+        release();
         continue;
       }
       // a part: the block that finishes last joins them, in their order
@@ -731,6 +785,7 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
         put_lse(mm, zz);
       }
+      release();
     }
   }
   tc_fence_before();

@@ -313,38 +313,5 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("sub.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-// 2^x of a pair on the FMA units, for -126 <= x <= 126 (smaller x counts as
-// -126): x = k + r with k the nearest integer (added and taken away with the
-// constant 1.5 * 2^23, whose low mantissa bits then hold k), 2^r on [-1/2, 1/2]
-// by a degree-5 polynomial fitted to the smallest relative error (2.2e-7 with
-// the roundings), and k added to the exponent field.  NaN gives a value that
-// is not finite or near the largest float32.
-__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
-  float a, b;
-  f2_unpack(x, a, b);
-  asm("max.NaN.f32 %0, %0, %1;\n" : "+f"(a) : "f"(-126.f));
-  asm("max.NaN.f32 %0, %0, %1;\n" : "+f"(b) : "f"(-126.f));
-  const uint64_t v = f2_pack(a, b), magic = f2_pack(12582912.f, 12582912.f);
-  const uint64_t t = f2_add(v, magic);
-  const uint64_t r = f2_sub(v, f2_sub(t, magic));
-  uint64_t p = f2_pack(0.001327647129073739f, 0.001327647129073739f);
-  p = f2_fma(p, r, f2_pack(0.009675540961325169f, 0.009675540961325169f));
-  p = f2_fma(p, r, f2_pack(0.05550713092088699f, 0.05550713092088699f));
-  p = f2_fma(p, r, f2_pack(0.24022120237350464f, 0.24022120237350464f));
-  p = f2_fma(p, r, f2_pack(0.6931469440460205f, 0.6931469440460205f));
-  p = f2_fma(p, r, f2_pack(1.0000001192092896f, 1.0000001192092896f));
-  float p0, p1, t0, t1;
-  f2_unpack(p, p0, p1);
-  f2_unpack(t, t0, t1);
-  p0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-  p1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
-  return f2_pack(p0, p1);
-}
 
 }  // namespace fl
