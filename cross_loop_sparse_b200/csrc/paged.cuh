@@ -54,6 +54,12 @@ __device__ __forceinline__ PgSeq pg_seq(const PgArgs& g, int b) {
   return s;
 }
 
+// a / b, in 32 bits where both fit (a 64-bit division is a hundred instructions).
+__device__ __forceinline__ long long pg_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // bf16 / fp16 as a template parameter: BF = 1 bf16, 0 fp16.
 template <int BF>
 __device__ __forceinline__ uint32_t pg_pack2(float lo, float hi) {
@@ -70,20 +76,57 @@ __device__ __forceinline__ void pg_mma(float (&d)[4], const uint32_t (&a)[4], ui
 }
 
 // The scratch of the paged attention.  A block that takes a cut of the column
-// line holds at most two items that are not whole, the first and the last.
-constexpr int kPgSms = 148;  // blocks of the tile kernel at most
-struct PgScratch {
-  uint32_t* tile_tickets;  // [2 * kPgSms * 2] arrivals of an item's parts, zeroed by the call
-  float2* tile_mz;         // [2 * kPgSms, 256] (m, z)
-  float* tile_n;           // [2 * kPgSms, 256, head_dim]
-  size_t ticket_bytes, total;
+// line holds at most two items that are not whole, the first and the last, and
+// at most one whose part 0 it has; of that one it leaves a record.
+constexpr int kPgSms = 148;        // blocks of the tile kernel at most; the few-row kernel runs two an SM
+constexpr int kPgTileRows = 256;   // rows of a slot of the tile kernel
+struct PgCut {
+  int parts, slot0;    // parts < 2: no item to join
+  int h, q0, n, r0;    // key head, the request's first row and rows, first packed row
+  int pad[2];
 };
+struct PgScratch {
+  PgCut* tile_cuts;  // [kPgSms]
+  float2* tile_mz;   // [2 * kPgSms, 256] (m, z)
+  float4* tile_n;    // [2 * kPgSms, head_dim / 4, 256]
+  PgCut* row_cuts;   // [2 * kPgSms]; NULL: the few-row kernel takes whole requests
+  float2* row_mz;    // [4 * kPgSms, 32]
+  float4* row_n;     // [4 * kPgSms, 32, head_dim / 4]
+  size_t total;
+};
+
+// The kernels of one call overlap: a later one is launched when all blocks of
+// the one before have started, and waits for its end only where it reads what
+// that wrote.  A kernel that needs nothing of the one before still waits at
+// its end, so that its own end means that everything before has ended.
+__device__ __forceinline__ void pg_launch_next() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void pg_wait_for_launch_before() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+template <typename Kernel, typename... Args>
+inline int pg_launch_early(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? FLASHLOOP_OK : FLASHLOOP_ERR_CUDA;
+}
 
 // Requests of at most this many packed rows (rows x group) are the few-row
 // kernel's, which reads the cache once for 32 of them; longer ones the tile kernel's.
 constexpr int kPgFewRows = 32;
 
-int launch_pg_rows(const PgArgs& g, int dh, int bf16, cudaStream_t stream);
-int launch_pg_tile(const PgArgs& g, int dh, int bf16, int few, const PgScratch& ws, cudaStream_t stream);
+// Tables of at most this many columns are not cut: whole requests are a few
+// microseconds' work, and a cut costs a second kernel.
+constexpr int kPgShort = 512;
+
+int launch_pg_rows(const PgArgs& g, int dh, int bf16, const PgScratch& ws, cudaStream_t stream);
+// early: behind the few-row kernel of the same call
+int launch_pg_tile(const PgArgs& g, int dh, int bf16, int few, const PgScratch& ws, bool early, cudaStream_t stream);
+int launch_pg_join(const PgArgs& g, int dh, int bf16, const PgScratch& ws, bool tiles, cudaStream_t stream);
 
 }  // namespace fl

@@ -86,12 +86,17 @@ static PgScratch pg_scratch(const flashloop_paged_params* p, void* base) {
     off = align256(off + bytes);
     return at;
   };
-  const size_t slots = 2 * kPgSms;
-  const bool tiles = (long long)p->max_new * (p->n_heads / p->n_kv_heads) > kPgFewRows;
-  w.ticket_bytes = slots * 2 * sizeof(uint32_t);
-  w.tile_tickets = ws_ptr<uint32_t>(base, take(w.ticket_bytes));
-  w.tile_mz = ws_ptr<float2>(base, take(tiles ? slots * 256 * sizeof(float2) : 0));
-  w.tile_n = ws_ptr<float>(base, take(tiles ? slots * 256 * (size_t)p->head_dim * sizeof(float) : 0));
+  const size_t slots = 2 * kPgSms, row_slots = 4 * kPgSms, dh = (size_t)p->head_dim;
+  if ((long long)p->max_new * (p->n_heads / p->n_kv_heads) > kPgFewRows) {
+    w.tile_cuts = ws_ptr<PgCut>(base, take(kPgSms * sizeof(PgCut)));
+    w.tile_mz = ws_ptr<float2>(base, take(slots * kPgTileRows * sizeof(float2)));
+    w.tile_n = ws_ptr<float4>(base, take(slots * kPgTileRows * dh * sizeof(float)));
+  }
+  if ((long long)p->max_blocks * p->page_size > kPgShort) {
+    w.row_cuts = ws_ptr<PgCut>(base, take(2 * kPgSms * sizeof(PgCut)));
+    w.row_mz = ws_ptr<float2>(base, take(row_slots * kPgFewRows * sizeof(float2)));
+    w.row_n = ws_ptr<float4>(base, take(row_slots * kPgFewRows * dh * sizeof(float)));
+  }
   w.total = off;
   return w;
 }
@@ -176,15 +181,16 @@ int flashloop_prompt_attn(const flashloop_paged_params* p, const flashloop_rows*
   g.v = {static_cast<const uint16_t*>(v->data), 0, v->stride_token, v->stride_head};
   const int bf16 = p->dtype == FLASHLOOP_DTYPE_BF16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!pg_tma_ok(g, 1)) return launch_pg_rows(g, p->head_dim, bf16, s);
-  return launch_pg_tile(g, p->head_dim, bf16, 0, PgScratch{}, s);
+  if (!pg_tma_ok(g, 1)) return launch_pg_rows(g, p->head_dim, bf16, PgScratch{}, s);
+  return launch_pg_tile(g, p->head_dim, bf16, 0, PgScratch{}, false, s);
 }
 
 size_t flashloop_paged_attn_workspace_bytes(const flashloop_paged_params* p) {
   if (pg_check_sizes(p) != FLASHLOOP_OK || pg_check_pages(p) != FLASHLOOP_OK ||
       pg_check_heads(p, true) != FLASHLOOP_OK)
     return 0;
-  return pg_scratch(p, nullptr).total;
+  const size_t n = pg_scratch(p, nullptr).total;
+  return n > 0 ? n : 16;
 }
 
 int flashloop_paged_attn(const flashloop_paged_params* p, const flashloop_rows* q, const flashloop_pages* k_cache,
@@ -213,20 +219,20 @@ int flashloop_paged_attn(const flashloop_paged_params* p, const flashloop_rows* 
   g.v = pg_pages(v_cache);
   const int bf16 = p->dtype == FLASHLOOP_DTYPE_BF16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool tiles = (long long)g.max_new * g.G > kPgFewRows && pg_tma_ok(g, p->n_pages);
   const PgScratch ws = pg_scratch(p, workspace);
-  if (tiles) {
-    FL_TRY(cudaMemsetAsync(ws.tile_tickets, 0, ws.ticket_bytes, s));
-    PgArgs few = g;
-    few.max_new = kPgFewRows / g.G;
-    few.skip_longer = 1;
-    if (few.max_new > 0) {
-      rc = launch_pg_rows(few, p->head_dim, bf16, s);
-      if (rc != FLASHLOOP_OK) return rc;
-    }
-    return launch_pg_tile(g, p->head_dim, bf16, kPgFewRows, ws, s);
+  if ((long long)g.max_new * g.G <= kPgFewRows) {
+    rc = launch_pg_rows(g, p->head_dim, bf16, ws, s);
+    return rc != FLASHLOOP_OK ? rc : launch_pg_join(g, p->head_dim, bf16, ws, false, s);
   }
-  return launch_pg_rows(g, p->head_dim, bf16, s);
+  if (!pg_tma_ok(g, p->n_pages)) return launch_pg_rows(g, p->head_dim, bf16, PgScratch{}, s);
+  PgArgs few = g;
+  few.max_new = kPgFewRows / g.G;
+  few.skip_longer = 1;
+  PgScratch rows_ws = ws;
+  if (few.max_new > 0) rc = launch_pg_rows(few, p->head_dim, bf16, ws, s);
+  else rows_ws.row_cuts = nullptr;  // no request has so few packed rows
+  if (rc == FLASHLOOP_OK) rc = launch_pg_tile(g, p->head_dim, bf16, kPgFewRows, ws, few.max_new > 0, s);
+  return rc != FLASHLOOP_OK ? rc : launch_pg_join(g, p->head_dim, bf16, rows_ws, true, s);
 }
 
 }  // extern "C"

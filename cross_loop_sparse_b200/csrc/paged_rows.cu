@@ -13,6 +13,13 @@
 //   p = 2^(s - m), z = sum p, N = sum p v, o = N / z, lse = (m + log2 z) ln 2.
 // Scores, sums and N are float32; p is rounded to the values' type, since the
 // matrix product takes one type.
+//
+// Bound by HBM: a column costs 4 * head_dim bytes and few instructions.  With
+// scratch, the stages of all requests and key heads are one line that is cut
+// into equal lengths, one a block and two blocks an SM, so that requests of any
+// mix of lengths load the SMs alike; what a border cuts leaves float32 N, m and z
+// in scratch, which another kernel joins.  Short tables need no cut and no
+// scratch: a block a request, key head and row tile.
 #include <type_traits>
 
 #include "paged.cuh"
@@ -27,27 +34,44 @@ template <int DH, int MT>
 struct PrCfg {
   static constexpr int kRows = 16 * MT;
   static constexpr int kTile = 16 * DH * 2;  // bytes of a warp's K (or V) slice of a stage
-  static constexpr int kStages = 3;
+  static constexpr int kStages = DH == 128 ? 3 : 6;
   static constexpr int kWarpRing = kStages * 2 * kTile;
   static constexpr int kPitch = DH + 8;  // floats, of the joined numerators
   static constexpr int kJoin = 4 * kRows * (kPitch + 2) * 4;
   static constexpr int kSmem = 4 * kWarpRing > kJoin ? 4 * kWarpRing : kJoin;
 };
 
+constexpr int kPrMinUnits = 4;  // units a block takes at least when the line is cut
+// Units of an item beside its stages: what starting and joining it costs, as
+// much as some stages do.  Without them a block that gets dozens of short
+// requests ends long after the others.
+constexpr int kPrStart = 6;
+
+struct PrArgs {
+  PgArgs g;
+  PgCut* cuts;      // [grid]; NULL: blocks take whole row tiles
+  float2* part_mz;  // [2 * grid, 32]
+  float4* part_n;   // [2 * grid, 32, DH / 4]
+};
+
+// Columns [c0, c1) of the rows from r0 on of one request and key head.
+struct PrItem {
+  int b, h, q0, n, L, r0, c0, c1;
+  int slot, parts;  // scratch slot, number of parts of the whole item (1 = this is all)
+};
+
 template <int DH, int BF, int MT>
-__global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PgArgs g) {
+__device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_t* smem) {
   using C = PrCfg<DH, MT>;
   constexpr int kPieces = DH / 8;
-  extern __shared__ __align__(128) uint8_t smem[];
+  const PgArgs& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.z, h = blockIdx.y, r0 = blockIdx.x * C::kRows;
-  const PgSeq s = pg_seq(g, b);
+  const int b = s.b, h = s.h, r0 = s.r0;
   const int rows = s.n * g.G;
-  if (r0 >= rows) return;
   const int shift = g.table ? g.shift : 31;
-  const int off = s.L - s.n;                                      // row i sees j <= off + i
-  const int ncols = max(0, off + (min(rows, r0 + C::kRows) - 1) / g.G + 1);  // of the tile's last row
-  const int free_cols = off + r0 / g.G + 1;                       // columns that every row sees
+  const int off = s.L - s.n;                 // row i sees j <= off + i
+  const int free_cols = off + r0 / g.G + 1;  // columns that every row sees
+  const int ncols = s.c1;
   uint8_t* ring = smem + warp * C::kWarpRing;
 
   // queries: the A fragments of every k step
@@ -69,11 +93,11 @@ __global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PgArgs g) {
       }
     }
 
-  const int stages = (ncols + kPrCols - 1) / kPrCols;
+  const int stages = (ncols - s.c0 + kPrCols - 1) / kPrCols;
   // the page of this warp's slice of stages [32 i, 32 i + 32): lane l holds stage 32 i + l
   auto pages_of = [&](int st) -> int {
-    const int col = st * kPrCols + warp * 16;
-    if (col >= ncols) return -1;
+    const int col = s.c0 + st * kPrCols + warp * 16;
+    if (st >= stages || col >= ncols) return -1;
     if (!g.table) return 0;
     const int page = g.table[(size_t)b * g.max_blocks + (col >> shift)];
     if (page < 0 || page >= g.n_pages) {
@@ -91,7 +115,7 @@ __global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PgArgs g) {
         pages_next = pages_of(st + 32 + lane);
       }
       const int page = __shfl_sync(0xffffffffu, pages, st & 31);
-      const int c0 = st * kPrCols + warp * 16;
+      const int c0 = s.c0 + st * kPrCols + warp * 16;
       const int in0 = g.table ? (c0 & ((1 << shift) - 1)) : c0;
       uint8_t* dst = ring + (st % C::kStages) * 2 * C::kTile;
       const uint16_t* kb = g.k.p + (page > 0 ? page : 0) * g.k.sp + (row0 + in0) * g.k.st + h * g.k.sh;
@@ -108,7 +132,7 @@ __global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PgArgs g) {
     cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < C::kStages - 1; ++i) load(i);
+  for (int i = 0; i < C::kStages; ++i) load(i);
 
   float o[MT][DH / 8][4];
   float m[MT][2], z[MT][2];
@@ -123,12 +147,11 @@ __global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PgArgs g) {
   }
 
   for (int st = 0; st < stages; ++st) {
-    load(st + C::kStages - 1);
     cp_async_wait<C::kStages - 1>();
     __syncwarp();
     const uint8_t* kt = ring + (st % C::kStages) * 2 * C::kTile;
     const uint8_t* vt = kt + C::kTile;
-    const int c0 = st * kPrCols + warp * 16;
+    const int c0 = s.c0 + st * kPrCols + warp * 16;
     float sc[MT][2][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -203,6 +226,7 @@ __global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PgArgs g) {
       }
     }
     __syncwarp();
+    load(st + C::kStages);
   }
   cp_async_wait<0>();
 
@@ -249,20 +273,134 @@ __global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PgArgs g) {
       acc.z += f * x.z;
       acc.w += f * x.w;
     }
+    if (s.parts > 1) {
+      const size_t at = (size_t)s.slot * kPgFewRows + r;
+      __stcg(a.part_n + at * (DH / 4) + c / 4, acc);
+      if (c == 0) __stcg(a.part_mz + at, make_float2(mm, zz));
+      continue;
+    }
     const int tok = (r0 + r) / g.G, hq = h * g.G + (r0 + r) - tok * g.G;
     const float inv = zz == 0.f ? 0.f : 1.f / zz;
-    uint2 out = make_uint2(pg_pack2<BF>(acc.x * inv, acc.y * inv), pg_pack2<BF>(acc.z * inv, acc.w * inv));
-    *reinterpret_cast<uint2*>(g.o.p + (s.q0 + tok) * g.o.st + hq * g.o.sh + c) = out;
+    *reinterpret_cast<uint2*>(g.o.p + (s.q0 + tok) * g.o.st + hq * g.o.sh + c) =
+        make_uint2(pg_pack2<BF>(acc.x * inv, acc.y * inv), pg_pack2<BF>(acc.z * inv, acc.w * inv));
     if (g.lse && c == 0)
       g.lse[(size_t)hq * g.max_tokens + s.q0 + tok] = zz == 0.f ? -INFINITY : (mm + log2f(zz)) * kPgLn2;
   }
 }
 
-int launch_pg_rows(const PgArgs& g, int dh, int bf16, cudaStream_t stream) {
+// Units of one key head of request s; a request whose rows see nothing still has them written.
+__device__ __forceinline__ int pr_units(const PgSeq& s) {
+  return s.n > 0 ? kPrStart + max(1, (s.L + kPrCols - 1) / kPrCols) : 0;
+}
+
+template <int DH, int BF, int MT>
+__global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PrArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int s_b;
+  __shared__ long long s_sum[kPrThreads / 32], s_at;
+  pg_launch_next();
+  const PgArgs& g = a.g;
+  if (a.cuts == nullptr) {
+    const PgSeq q = pg_seq(g, blockIdx.z);
+    const int rows = q.n * g.G, r0 = blockIdx.x * PrCfg<DH, MT>::kRows;
+    if (r0 >= rows) return;
+    const int seen = q.L - q.n + (min(rows, r0 + PrCfg<DH, MT>::kRows) - 1) / g.G + 1;  // by the tile's last row
+    PrItem it{(int)blockIdx.z, (int)blockIdx.y, q.q0, q.n, q.L, r0, 0, max(0, seen), 0, 1};
+    pr_item<DH, BF, MT>(a, it, smem);
+    return;
+  }
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // a thread's request of the chunk at b0, and sums over the chunk: inclusive and whole
+  PgSeq q;
+  long long incl, whole;
+  auto chunk = [&](int b0) {
+    q = {0, 0, 0};
+    if (b0 + tid < g.B) q = pg_seq(g, b0 + tid);
+    incl = pr_units(q);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    whole = 0;
+#pragma unroll
+    for (int w = 0; w < kPrThreads / 32; ++w) {
+      if (w < warp) incl += s_sum[w];
+      whole += s_sum[w];
+    }
+  };
+  long long total = 0;
+  for (int b0 = 0; b0 < g.B; b0 += kPrThreads) {
+    chunk(b0);
+    total += whole;
+  }
+  total *= g.Hk;
+  if (tid == 0) a.cuts[blockIdx.x].parts = 0;
+  const long long per = max((long long)kPrMinUnits, pg_div(total + gridDim.x - 1, gridDim.x));
+  long long x = blockIdx.x * per;
+  const long long x1 = min(total, x + per);
+  if (x >= x1) return;
+  // the request that holds x
+  long long base = 0;
+  for (int b0 = 0; b0 < g.B; b0 += kPrThreads) {
+    if (g.B > kPrThreads) chunk(b0);
+    const long long first = base + (incl - pr_units(q)) * g.Hk;
+    if (x >= first && x < base + incl * g.Hk) {
+      s_b = b0 + tid;
+      s_at = first;
+    }
+    base += whole * g.Hk;
+    if (x < base) break;
+  }
+  __syncthreads();
+  int b = s_b;
+  long long at = s_at;  // the request's first unit
+  while (x < x1) {
+    q = pg_seq(g, b);
+    const int u = pr_units(q);
+    while (x < x1 && x < at + (long long)u * g.Hk) {
+      PrItem it{};
+      it.b = b;
+      it.h = (int)pg_div(x - at, u);
+      it.q0 = q.q0;
+      it.n = q.n;
+      it.L = q.L;
+      const long long u1 = at + (long long)(it.h + 1) * u, end = min(u1, x1);
+      const long long s0 = u1 - u + kPrStart;  // its first stage
+      if (end <= s0) {  // the next block has its stages
+        x = end;
+        break;
+      }
+      it.c0 = (int)max(0ll, x - s0) * kPrCols;
+      it.c1 = min(q.L, (int)(end - s0) * kPrCols);
+      const long long fc = pg_div(s0, per), lc = pg_div(u1 - 1, per);
+      it.parts = (int)(lc - fc) + 1;
+      // the first item of a block has its slot 0, the last, if it goes on behind the block, slot 1
+      it.slot = blockIdx.x * 2 + (fc == blockIdx.x && s0 != fc * per);
+      if (it.parts > 1 && fc == blockIdx.x && tid == 0)
+        a.cuts[blockIdx.x] = PgCut{it.parts, it.slot, it.h, it.q0, it.n, 0, {0, 0}};
+      // a request of one row tile does half of the products
+      if (MT == 2 && q.n * g.G <= 16) pr_item<DH, BF, 1>(a, it, smem);
+      else pr_item<DH, BF, MT>(a, it, smem);
+      __syncthreads();  // shared memory goes to the next item
+      x = end;
+    }
+    at += (long long)u * g.Hk;
+    ++b;
+  }
+}
+
+int launch_pg_rows(const PgArgs& g, int dh, int bf16, const PgScratch& ws, cudaStream_t stream) {
+  PrArgs a{g, ws.row_cuts, ws.row_mz, ws.row_n};
   const long long rows = (long long)g.max_new * g.G;
   auto go = [&](auto kernel, int rt, int smem) -> int {
     FL_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    kernel<<<dim3((unsigned)((rows + rt - 1) / rt), g.Hk, g.B), kPrThreads, smem, stream>>>(g);
+    dim3 grid((unsigned)((rows + rt - 1) / rt), g.Hk, g.B);
+    if (a.cuts) grid = dim3(2 * kPgSms);  // each leaves a record
+    kernel<<<grid, kPrThreads, smem, stream>>>(a);
     return launch_status();
   };
   auto pick = [&](auto dhc) -> int {

@@ -42,9 +42,8 @@
 // Work: without scratch (prompts) an item is a whole row pair, dealt to and fro
 // from a list that begins with the longest.  With scratch (paged) the column tiles of all items are one
 // line that is cut into equal lengths, one a block, so that few rows over a
-// long cache still use every SM; an item cut by a border is joined by the
-// block that finishes last (float32 N, m, z in scratch, in the order of its
-// parts, so that results do not depend on timing).
+// long cache still use every SM; an item cut by a border leaves float32 N, m
+// and z in scratch, which another kernel joins.
 //
 // Every wait is bounded; one that gives up sets FLASHLOOP_DEVERR_TIMEOUT, and the
 // block unwinds.
@@ -84,16 +83,16 @@ struct PtCfg {
 struct PtItem {
   int valid, b, h, q0, n, L, r0;
   int t0, t1;            // column tiles
-  int slot, slot0, parts, part;  // scratch slot of this part, of part 0, number of parts (1 = whole)
+  int slot, parts;       // scratch slot, number of parts of the whole item (1 = this is all)
 };
 
 struct PtArgs {
   PgArgs g;
   int few;        // requests with at most this many packed rows are another kernel's
   int box_shift;  // tokens of a TMA box: 1 << box_shift
-  uint32_t* tickets;  // [2 * grid * 2], zero; NULL: items are whole
-  float2* part_mz;    // [2 * grid, 256]
-  float* part_n;      // [2 * grid, 256, DH]
+  PgCut* cuts;      // [grid]; NULL: items are whole
+  float2* part_mz;  // [2 * grid, 256]
+  float4* part_n;   // [2 * grid, DH / 4, 256]
 };
 
 __device__ __forceinline__ int pt_pairs(const PtArgs& a, int n) {
@@ -132,7 +131,7 @@ __device__ __forceinline__ void pt_schedule(const PtArgs& a, int lane, Emit emit
     if (b0 + lane < g.B) s = pg_seq(g, b0 + lane);
     np = pt_pairs(a, s.n);
   };
-  if (a.tickets == nullptr) {
+  if (a.cuts == nullptr) {
     // whole items, dealt out to and fro (block c takes items c, 2 grid - 1 - c, 2 grid + c, ...) from
     // a list that begins with the longest: those of 2^c column tiles and more, c falling, and
     // within a class and request the last rows first
@@ -191,21 +190,26 @@ __device__ __forceinline__ void pt_schedule(const PtArgs& a, int lane, Emit emit
     }
     return u;
   };
-  long long total = 0;
+  long long total = 0, hu = 0;
   for (int b0 = 0; b0 < g.B; b0 += 32) {
     chunk(b0);
-    long long u = head_units() * g.Hk;
+    hu = head_units();
+    long long u = hu * g.Hk;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(kAll, u, o);
     total += u;
   }
-  const long long per = max((long long)kPtMinUnits, (total + gridDim.x - 1) / gridDim.x);
+  if (lane == 0) a.cuts[blockIdx.x].parts = 0;
+  const long long per = max((long long)kPtMinUnits, pg_div(total + gridDim.x - 1, gridDim.x));
   long long x = blockIdx.x * per;
   const long long x1 = min(total, x + per);
   long long base = 0;
   for (int b0 = 0; b0 < g.B && x < x1; b0 += 32) {
-    chunk(b0);
-    const long long hu = head_units(), mine = hu * g.Hk;
+    if (g.B > 32) {
+      chunk(b0);
+      hu = head_units();
+    }
+    const long long mine = hu * g.Hk;
     long long end = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -224,7 +228,7 @@ __device__ __forceinline__ void pt_schedule(const PtArgs& a, int lane, Emit emit
       it.q0 = __shfl_sync(kAll, s.q0, src);
       it.n = __shfl_sync(kAll, s.n, src);
       it.L = __shfl_sync(kAll, s.L, src);
-      it.h = (int)((x - b_at) / head);
+      it.h = (int)pg_div(x - b_at, head);
       long long at = b_at + it.h * head;  // the head's first unit; pairs follow, long rows first
       // the pair that holds x: prefix sums over 32 pairs at a time
       for (int i0 = 0; i0 < n_p; i0 += 32) {
@@ -246,11 +250,12 @@ __device__ __forceinline__ void pt_schedule(const PtArgs& a, int lane, Emit emit
         it.r0 = (n_p - 1 - (i0 + hl)) * kPtPair;
         it.t0 = (int)(x - u0);
         it.t1 = (int)(min(u1, x1) - u0);
-        const long long fc = u0 / per, lc = (u1 - 1) / per;
+        const long long fc = pg_div(u0, per), lc = pg_div(u1 - 1, per);
         it.parts = (int)(lc - fc) + 1;
-        it.part = (int)(blockIdx.x - fc);
-        it.slot0 = (int)(fc * 2 + (u0 % per != 0));
-        it.slot = it.part == 0 ? it.slot0 : (int)(blockIdx.x * 2);
+        // the first item of a block has its slot 0, the last, if it goes on behind the block, slot 1
+        it.slot = blockIdx.x * 2 + (fc == blockIdx.x && u0 != fc * per);
+        if (it.parts > 1 && fc == blockIdx.x && lane == 0)
+          a.cuts[blockIdx.x] = PgCut{it.parts, it.slot, it.h, it.q0, it.n, it.r0, {0, 0}};
         x = min(u1, x1);
         break;
       }
@@ -312,12 +317,12 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   uint64_t* tail = item_empty + 2;           // [1] bytes of a V tile whose last rows are cleared
   uint64_t* fin = tail + 1;                  // [1] every MMA of both issuers completed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
-  int* last_flag = reinterpret_cast<int*>(tmem_slot + 2);  // [x]
   PtItem* items = reinterpret_cast<PtItem*>(tmem_slot + 4);  // [2]
   static_assert((2 * C::kStages + 24) * 8 + 16 + 2 * sizeof(PtItem) <= 512, "barriers");
   uint8_t* ring = smem + C::kRingOff;
   const PgArgs& g = a.g;
 
+  pg_launch_next();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -558,7 +563,6 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   } else if (warp >= kPtWarpQ) {
     // ------------------------------------------------------------ queries
     pt_regs_dec<kPtRegsRest>();
-    const int tid = threadIdx.x - kPtWarpQ * 32;
     constexpr int kPieces = DH / 8;
     bool ok = true;
     PtItem it;
@@ -569,15 +573,21 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           ok = false;
           break;
         }
-        uint8_t* dst = smem + x * C::kQBytes;
-#pragma unroll 4
-        for (int i = tid; i < kPtRows * kPieces; i += 128) {
-          const int row = i / kPieces, c = i % kPieces;
-          const int r = it.r0 + x * kPtRows + row;
-          const int tok = r / g.G;
-          const uint16_t* src = g.q.p;
-          if (r < rows) src += (it.q0 + tok) * g.q.st + (long long)(it.h * g.G + r - tok * g.G) * g.q.sh + c * 8;
-          cp_async16(dst + (c >> 3) * C::kQChunk + row * 128 + (((c & 7) ^ (row & 7)) << 4), src, r < rows ? 16 : 0);
+        // a warp brings 32 rows, 16 bytes a lane; lane l knows where row l lies
+        const int mine = it.r0 + x * kPtRows + (warp - kPtWarpQ) * 32 + lane;
+        const uint16_t* at = nullptr;
+        if (mine < rows) {
+          const int tok = mine / g.G;
+          at = g.q.p + (it.q0 + tok) * g.q.st + (long long)(it.h * g.G + mine - tok * g.G) * g.q.sh;
+        }
+        const unsigned long long mine_at = reinterpret_cast<unsigned long long>(at);
+        const int c = lane % kPieces;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int from = i * (32 / kPieces) + lane / kPieces, row = (warp - kPtWarpQ) * 32 + from;
+          const unsigned long long src = __shfl_sync(0xffffffffu, mine_at, from);
+          cp_async16(smem + x * C::kQBytes + (c >> 3) * C::kQChunk + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                     src ? reinterpret_cast<const uint16_t*>(src) + c * 8 : g.q.p, src ? 16 : 0);
         }
         cp_async_wait_all();
         fence_proxy_async_smem();
@@ -726,9 +736,10 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         if (it.parts == 1) {
           put(cc, v, inv);
         } else if (live && my > 0) {
-          float4* d = reinterpret_cast<float4*>(a.part_n + prow * DH + cc);
+          float4* d = a.part_n + ((size_t)it.slot * (DH / 4) + cc / 4) * kPtPair + x * kPtRows + row;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) __stcg(d + e, make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
+          for (int e = 0; e < 8; ++e)
+            __stcg(d + e * kPtPair, make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
         }
       }
       tc_fence_before();
@@ -739,52 +750,8 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         release();
         continue;
       }
-      // a part: the block that finishes last joins them, in their order
-      __stcg(a.part_mz + prow, make_float2(my > 0 ? m_ref : -INFINITY, my > 0 ? z : 0.f));
-      __threadfence();
-      named_bar_sync(1 + x, kPtRows);
-      if (row == 0) {
-        const uint32_t done = atomicAdd(&a.tickets[it.slot0 * 2 + x], 1u);
-        __threadfence();
-        last_flag[x] = done == (uint32_t)(it.parts - 1);
-      }
-      named_bar_sync(1 + x, kPtRows);
-      if (last_flag[x]) {
-        __threadfence();
-        const size_t row0 = (size_t)it.slot0 * kPtPair + x * kPtRows + row;
-        // part i > 0 lies in its block's first slot
-        const size_t block0 = (size_t)(it.slot0 >> 1);
-        auto prow_of = [&](int i) { return i == 0 ? row0 : ((block0 + i) * 2) * kPtPair + x * kPtRows + row; };
-        float mm = -INFINITY, zz = 0.f;
-        for (int i = 0; i < it.parts; ++i) mm = fmaxf(mm, __ldcg(a.part_mz + prow_of(i)).x);
-        for (int i = 0; i < it.parts; ++i) {
-          const float2 mz = __ldcg(a.part_mz + prow_of(i));
-          if (mz.x != -INFINITY || mz.y != 0.f) zz += mz.y * ex2(mz.x - mm);
-        }
-        const float minv = zz == 0.f ? 0.f : 1.f / zz;
-#pragma unroll 1
-        for (int cc = 0; cc < DH; cc += 32) {
-          float v[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0.f;
-          for (int i = 0; i < it.parts; ++i) {
-            const float2 mz = __ldcg(a.part_mz + prow_of(i));
-            if (!live || (mz.x == -INFINITY && mz.y == 0.f)) continue;
-            const float f = ex2(mz.x - mm);
-            const float4* d = reinterpret_cast<const float4*>(a.part_n + prow_of(i) * DH + cc);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 n4 = __ldcg(d + e);
-              v[4 * e] += f * n4.x;
-              v[4 * e + 1] += f * n4.y;
-              v[4 * e + 2] += f * n4.z;
-              v[4 * e + 3] += f * n4.w;
-            }
-          }
-          put(cc, v, minv);
-        }
-        put_lse(mm, zz);
-      }
+      // a part: another kernel joins them
+      if (live) __stcg(a.part_mz + prow, make_float2(my > 0 ? m_ref : -INFINITY, my > 0 ? z : 0.f));
       release();
     }
   }
@@ -794,6 +761,7 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (threadIdx.x == 0) pg_wait_for_launch_before();
 }
 
 int at_sm_count();
@@ -825,12 +793,12 @@ static int pt_tmap(CUtensorMap* map, const PgPages& t, int bf16, uint64_t dh, ui
   return r == CUDA_SUCCESS ? FLASHLOOP_OK : FLASHLOOP_ERR_CUDA;
 }
 
-int launch_pg_tile(const PgArgs& g, int dh, int bf16, int few, const PgScratch& ws, cudaStream_t stream) {
+int launch_pg_tile(const PgArgs& g, int dh, int bf16, int few, const PgScratch& ws, bool early, cudaStream_t stream) {
   PtArgs a{};
   a.g = g;
   a.few = few;
   a.box_shift = g.table && g.shift < 7 ? g.shift : 7;
-  a.tickets = ws.tile_tickets;
+  a.cuts = ws.tile_cuts;
   a.part_mz = ws.tile_mz;
   a.part_n = ws.tile_n;
   const uint64_t tokens = g.table ? 1ull << g.shift : (uint64_t)g.max_tokens;
@@ -840,14 +808,15 @@ int launch_pg_tile(const PgArgs& g, int dh, int bf16, int few, const PgScratch& 
   int rc = pt_tmap(&tk, g.k, bf16, dh, tokens, g.Hk, pages, rows);
   if (rc == FLASHLOOP_OK) rc = pt_tmap(&tv, g.v, bf16, dh, tokens, g.Hk, pages, rows);
   if (rc != FLASHLOOP_OK) return rc;
-  int grid = at_sm_count();
-  if (grid > kPgSms) grid = kPgSms;
-  if (!a.tickets) {
+  int grid = kPgSms;  // in a cut, each leaves a record
+  if (!a.cuts) {
+    grid = at_sm_count();
     const long long items = (long long)g.Hk * (((long long)g.max_tokens * g.G + kPtPair - 1) / kPtPair + g.B);
     if (grid > items) grid = (int)items;
   }
   auto go = [&](auto kernel, int smem) -> int {
     FL_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    if (early) return pg_launch_early(kernel, dim3(grid), kPtThreads, smem, stream, tk, tv, a);
     kernel<<<grid, kPtThreads, smem, stream>>>(tk, tv, a);
     return launch_status();
   };
