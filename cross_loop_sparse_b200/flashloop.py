@@ -365,49 +365,61 @@ def flashloop_check_error_word(err_word, stream=None):
 
 
 # ----------------------------------------------------------------------------- many requests
-def _need(ok, fn, detail, status=-1):
-    if not ok:
-        raise FlashLoopError(fn, status, detail)
-
-
 def _vec(fn, name, t, n, dtype, dev):
-    """Address of a contiguous device vector of at least n elements."""
-    if t.dtype != dtype or not t.is_contiguous() or t.numel() < n or t.device != dev:
-        raise FlashLoopError(fn, -1, f"{name}: a contiguous {dtype} tensor of at least {n} elements on {dev}")
-    return t.data_ptr()
+    """Address of a contiguous vector of at least n elements on CUDA device dev (an index)."""
+    if t.dtype is dtype and t.get_device() == dev and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
+    raise FlashLoopError(fn, -1, f"{name}: a contiguous {dtype} tensor of at least {n} elements on cuda:{dev}, "
+                                 f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _rows(fn, name, t, shape, dtype, dev, written=False):
-    if t.shape != shape or t.dtype != dtype or t.device != dev:
-        raise FlashLoopError(fn, -1, f"{name}: {dtype} {tuple(shape)} on {dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
+    """flashloop_rows of [tokens, heads, head_dim]."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        raise FlashLoopError(fn, -1, f"{name}: {dtype} {shape} on cuda:{dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
     st, sh, se = t.stride()
-    _need(se == 1, fn, f"{name}: head_dim has to be contiguous")
-    _need(not written or ((st or shape[0] < 2) and (sh or shape[1] < 2)), fn, f"{name}: rows that overlap")
+    if se != 1:
+        raise FlashLoopError(fn, -1, f"{name}: head_dim has to be contiguous")
+    if written and not (st or shape[0] < 2) or written and not (sh or shape[1] < 2):
+        raise FlashLoopError(fn, -1, f"{name}: rows that overlap")
     return RowsC(t.data_ptr(), st, sh)
 
 
 def _pages(fn, name, t, p, dtype, dev, written=False):
+    """flashloop_pages of [n_pages, page_size, n_kv_heads, head_dim]."""
     shape = (p.n_pages, p.page_size, p.n_kv_heads, p.head_dim)
-    if t.shape != shape or t.dtype != dtype or t.device != dev:
-        raise FlashLoopError(fn, -1, f"{name}: {dtype} {shape} on {dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
-    st = t.stride()
-    _need(st[3] == 1, fn, f"{name}: head_dim has to be contiguous")
-    _need(not written or all(st[i] or shape[i] < 2 for i in range(3)), fn, f"{name}: pages that overlap")
-    return PagesC(t.data_ptr(), st[0], st[1], st[2])
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        raise FlashLoopError(fn, -1, f"{name}: {dtype} {shape} on cuda:{dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
+    sp, st, sh, se = t.stride()
+    if se != 1:
+        raise FlashLoopError(fn, -1, f"{name}: head_dim has to be contiguous")
+    if written and not all(x or n < 2 for x, n in zip((sp, st, sh), shape)):
+        raise FlashLoopError(fn, -1, f"{name}: pages that overlap")
+    return PagesC(t.data_ptr(), sp, st, sh)
 
 
 def _paged_dtype(fn, p):
-    _need(p.dtype in (0, 1), fn, "dtype", -2)
+    if p.dtype not in (0, 1):
+        raise FlashLoopError(fn, -2, f"dtype {p.dtype}")
     return torch.float16 if p.dtype else torch.bfloat16
+
+
+# The current stream's handle without a Stream object (a microsecond less a call) where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _launch(fn, dev, stream, *args):
     """Call into the library on the tensors' device, on its current stream by default."""
-    _need(dev.type == "cuda", fn, "tensors on a CUDA device")
-    if torch.cuda.current_device() != dev.index:
+    if dev < 0:
+        raise FlashLoopError(fn, -1, "tensors on a CUDA device")
+    if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
-            return _check(fn, getattr(_lib, fn)(*args, _stream(stream)))
-    return _check(fn, getattr(_lib, fn)(*args, _stream(stream)))
+            rc = getattr(_lib, fn)(*args, _stream(stream))
+    else:
+        rc = getattr(_lib, fn)(*args, _raw_stream(dev) if stream is None and _raw_stream else _stream(stream))
+    if rc:
+        raise FlashLoopError(fn, rc)
+    return rc
 
 
 def flashloop_paged_plan(params, kv_lens, new_lens, free_pages, n_free, block_table, cu, kv_lens_out, slot_map,
@@ -415,7 +427,7 @@ def flashloop_paged_plan(params, kv_lens, new_lens, free_pages, n_free, block_ta
     """Block tables, slot maps, positions and packed starts of the tokens that the requests
     append (see the header).  int32 tensors; block_table [batch, max_blocks] and n_free_out,
     kv_lens_out, cu [batch + 1], slot_map and positions [max_tokens] are written."""
-    fn, p, dev, i32 = "flashloop_paged_plan", params, kv_lens.device, torch.int32
+    fn, p, dev, i32 = "flashloop_paged_plan", params, kv_lens.get_device(), torch.int32
     B, T = max(p.batch, 0), max(p.max_tokens, 0)
     return _launch(fn, dev, stream, ctypes.byref(p), _vec(fn, "kv_lens", kv_lens, B, i32, dev),
                    _vec(fn, "new_lens", new_lens, B, i32, dev),
@@ -429,10 +441,11 @@ def flashloop_paged_plan(params, kv_lens, new_lens, free_pages, n_free, block_ta
 def flashloop_paged_kv_write(params, k, v, slot_map, k_cache, v_cache, err_word, stream=None):
     """Write k and v [max_tokens, n_kv_heads, head_dim] (params.dtype or float32) into the pages
     [n_pages, page_size, n_kv_heads, head_dim] of their slots."""
-    fn, p, dev = "flashloop_paged_kv_write", params, k_cache.device
+    fn, p, dev = "flashloop_paged_kv_write", params, k_cache.get_device()
     dt = _paged_dtype(fn, p)
     shape = (p.max_tokens, p.n_kv_heads, p.head_dim)
-    _need(k.dtype in PAGED_DTYPES, fn, f"k: {k.dtype}", -2)
+    if k.dtype not in PAGED_DTYPES:
+        raise FlashLoopError(fn, -2, f"k: {k.dtype}")
     kr, vr = _rows(fn, "k", k, shape, k.dtype, dev), _rows(fn, "v", v, shape, k.dtype, dev)
     kc, vc = _pages(fn, "k_cache", k_cache, p, dt, dev, True), _pages(fn, "v_cache", v_cache, p, dt, dev, True)
     return _launch(fn, dev, stream, ctypes.byref(p), ctypes.byref(kr), ctypes.byref(vr), PAGED_DTYPES[k.dtype],
@@ -443,7 +456,7 @@ def flashloop_paged_kv_write(params, k, v, slot_map, k_cache, v_cache, err_word,
 def flashloop_prompt_attn(params, q, k, v, cu, o, lse, err_word, stream=None):
     """Causal attention over packed prompts: q and o [max_tokens, n_heads, head_dim], k and v
     [max_tokens, n_kv_heads, head_dim], cu int32 [batch + 1], lse float32 [n_heads, max_tokens] or None."""
-    fn, p, dev = "flashloop_prompt_attn", params, q.device
+    fn, p, dev = "flashloop_prompt_attn", params, q.get_device()
     dt = _paged_dtype(fn, p)
     qs, ks = (p.max_tokens, p.n_heads, p.head_dim), (p.max_tokens, p.n_kv_heads, p.head_dim)
     qr, kr, vr = _rows(fn, "q", q, qs, dt, dev), _rows(fn, "k", k, ks, dt, dev), _rows(fn, "v", v, ks, dt, dev)
@@ -462,13 +475,14 @@ def flashloop_paged_attn(params, q, k_cache, v_cache, block_table, kv_lens, cu, 
                          stream=None):
     """Attention of the requests' new rows q [max_tokens, n_heads, head_dim] over their pages
     (block_table int32 [batch, max_blocks], kv_lens int32 [batch] with the new tokens counted)."""
-    fn, p, dev = "flashloop_paged_attn", params, q.device
+    fn, p, dev = "flashloop_paged_attn", params, q.get_device()
     dt = _paged_dtype(fn, p)
     qs = (p.max_tokens, p.n_heads, p.head_dim)
     qr, orr = _rows(fn, "q", q, qs, dt, dev), _rows(fn, "o", o, qs, dt, dev, True)
     kc, vc = _pages(fn, "k_cache", k_cache, p, dt, dev), _pages(fn, "v_cache", v_cache, p, dt, dev)
     i32 = torch.int32
-    _need(workspace.is_contiguous() and workspace.device == dev, fn, "workspace: contiguous, on the tensors' device")
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise FlashLoopError(fn, -1, "workspace: contiguous, on the tensors' device")
     return _launch(fn, dev, stream, ctypes.byref(p), ctypes.byref(qr), ctypes.byref(kc), ctypes.byref(vc),
                    _vec(fn, "block_table", block_table, p.batch * p.max_blocks, i32, dev),
                    _vec(fn, "kv_lens", kv_lens, p.batch, i32, dev), _vec(fn, "cu", cu, p.batch + 1, i32, dev),
