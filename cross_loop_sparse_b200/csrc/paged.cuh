@@ -30,6 +30,7 @@ struct PgArgs {
   float* lse;
   int32_t* err;
   float scale_log2;  // scale * log2(e) > 0: scores in log2 units
+  int o32;           // rows of o begin on 32 bytes: whole sectors are written
   int skip_longer;   // requests with more than max_new rows are another kernel's, not a fault
 };
 

@@ -116,6 +116,7 @@ static PgArgs pg_args(const flashloop_paged_params* p, const flashloop_rows* q, 
   g.lse = lse;
   g.err = err;
   g.scale_log2 = p->scale * kPgLog2e;
+  g.o32 = (reinterpret_cast<uintptr_t>(o->data) & 31) == 0 && o->stride_token % 16 == 0 && o->stride_head % 16 == 0;
   return g;
 }
 

@@ -1,69 +1,93 @@
 // Joins the items that a border of the column line has cut: the kernels that
 // took the parts left each row's N, m and z (m in log2 units) in scratch, and
 //   m = max m_k,  z = sum z_k 2^(m_k - m),  o = sum N_k 2^(m_k - m) / z,
-// the sums in the order of the parts.  A kernel of its own over all SMs: the
-// block that finishes last taking them instead cost 20 us for 8 parts of 256
-// rows, all from one SM's share of L2, and counters that each call had to
-// clear.  It is launched early and waits for the parts, so that its launch
-// costs next to nothing.  Few rows over a long cache have many parts, and each
-// is a trip to L2: a warp takes a row's m and z, a lane a part, and the threads
-// that a block's rows leave over share the parts of a numerator.
+// the sums in an order that the parts alone decide.  A kernel of its own over
+// all SMs: the block that finishes last taking them instead cost 20 us for 8
+// parts of 256 rows, all from one SM's share of L2, and counters that each call
+// had to clear.  It is launched early and waits for the parts.  What it costs are
+// three dependent trips to L2 (the record, m and z, N) and the numerators' bytes:
+// every lane has several loads under way, and the threads that few rows leave
+// over share the parts.
 #include "paged.cuh"
 
 namespace fl {
 
-constexpr int kPjRows = 32;  // rows a block
 constexpr int kPjThreads = 512;
-constexpr int kPjParts = 2 * kPgSms;  // an item has at most a part a block
+constexpr int kPjWarps = kPjThreads / 32;
+constexpr int kPjRows = 64;           // rows of a tile item a block takes
+constexpr int kPjParts = 2 * kPgSms;  // an item has at most a part a block of the few-row kernel
 
 struct PjArgs {
   PgArgs g;
-  const PgCut* tile_cuts;  // [kPgSms] or NULL
-  const PgCut* row_cuts;   // [2 * kPgSms] or NULL
+  const PgCut* tile_cuts;  // [kPgSms], four blocks each
+  const PgCut* row_cuts;   // [row_blocks], a block each, the first ones
+  int row_blocks;
   const float2* tile_mz;
   const float2* row_mz;
   const float4* tile_n;
   const float4* row_n;
-  int row_blocks;          // blocks of the few-row kernel's items come first
 };
+
+// The weight of a part in a row: none if it saw nothing of it (it has no numerator in scratch either).
+__device__ __forceinline__ float pj_weight(const float2& mz, float m) {
+  return mz.x == -INFINITY && mz.y == 0.f ? 0.f : mz.y != mz.y ? mz.y : ex2(mz.x - m);
+}
+
+template <int BF>
+__device__ __forceinline__ void pj_put(const PgArgs& g, const PgCut& c, int r, int c4, const float4& acc, float inv) {
+  const int tok = (c.r0 + r) / g.G, hq = c.h * g.G + (c.r0 + r) - tok * g.G;
+  *reinterpret_cast<uint2*>(g.o.p + (c.q0 + tok) * g.o.st + hq * g.o.sh + c4 * 4) =
+      make_uint2(pg_pack2<BF>(acc.x * inv, acc.y * inv), pg_pack2<BF>(acc.z * inv, acc.w * inv));
+}
+
+__device__ __forceinline__ void pj_axpy(float4& acc, float w, const float4& x) {
+  if (w == 0.f) return;
+  acc.x += w * x.x;
+  acc.y += w * x.y;
+  acc.z += w * x.z;
+  acc.w += w * x.w;
+}
 
 template <int DH, int BF>
 __global__ void __launch_bounds__(kPjThreads) pg_join_kernel(PjArgs a) {
+  constexpr int kC4 = DH / 4;
+  // weights [row][part]: 32 rows of up to kPjParts parts, or 64 of up to kPgSms
+  constexpr int kWeights = kPgFewRows * (kPjParts + 1) > kPjRows * (kPgSms + 1) ? kPgFewRows * (kPjParts + 1)
+                                                                             : kPjRows * (kPgSms + 1);
+  __shared__ float s_w[kWeights];
+  __shared__ float s_inv[kPjRows];  // 1 / z
+  __shared__ float4 s_acc[kPjThreads];
   pg_wait_for_launch_before();
   const PgArgs& g = a.g;
-  const bool few = (int)blockIdx.x < a.row_blocks;
-  const int i0 = few ? blockIdx.x : blockIdx.x - a.row_blocks;
-  const PgCut c = few ? a.row_cuts[i0] : a.tile_cuts[i0 / (kPgTileRows / kPjRows)];
-  if (c.parts < 2) return;
-  const int first = few ? 0 : (i0 % (kPgTileRows / kPjRows)) * kPjRows;  // row within the slot
-  const int rows = c.n * g.G - c.r0;                                     // rows of the item, maybe more than the slot's
-  if (first >= rows) return;
-  const int slot_rows = few ? kPgFewRows : kPgTileRows;
-  const float2* mz_of = (few ? a.row_mz : a.tile_mz);
-  const float4* n_of = (few ? a.row_n : a.tile_n);
-  // weight of each part in a row, and 1 / z
-  __shared__ float s_w[kPjRows][kPjParts + 1];
-  __shared__ float s_inv[kPjRows];
-  __shared__ float4 s_acc[kPjThreads];
-  const int live = min(rows - first, kPjRows);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool few = (int)blockIdx.x < a.row_blocks;
+  const int tile = blockIdx.x - a.row_blocks;
+  const PgCut c = few ? a.row_cuts[blockIdx.x] : a.tile_cuts[tile / (kPgTileRows / kPjRows)];
+  if (c.parts < 2) return;
+  const int slot_rows = few ? kPgFewRows : kPgTileRows;
+  const int first = few ? 0 : (tile % (kPgTileRows / kPjRows)) * kPjRows;
+  const int live = min(min(c.n * g.G - c.r0, slot_rows) - first, kPjRows);
+  if (live <= 0) return;
+  const int pitch = c.parts | 1;
   // part i > 0 lies in its block's first slot
   auto slot = [&](int i) { return (size_t)(i == 0 ? c.slot0 : (c.slot0 & ~1) + 2 * i); };
-  for (int r = warp; r < live; r += kPjThreads / 32) {
+  const float2* mz_of = (few ? a.row_mz : a.tile_mz) + first;
+  // rows' weights: `lanes` lanes a row, as many as there are parts or a warp
+  const int lanes = c.parts > 16 ? 32 : c.parts > 8 ? 16 : c.parts > 4 ? 8 : 4;
+  for (int r0 = 0; r0 < live; r0 += kPjWarps * (32 / lanes)) {
+    const int r = r0 + warp * (32 / lanes) + lane / lanes, k0 = lane % lanes;
+    const bool on = r < live;
     float m = -INFINITY, z = 0.f;
-    for (int k = lane; k < c.parts; k += 32) m = fmaxf(m, __ldcg(mz_of + slot(k) * slot_rows + first + r).x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int k = lane; k < c.parts; k += 32) {
-      const float2 mz = __ldcg(mz_of + slot(k) * slot_rows + first + r);
-      // a part that saw nothing of the row has no weight, and no numerator in scratch
-      const float w = mz.x == -INFINITY && mz.y == 0.f ? 0.f : ex2(mz.x - m);
-      s_w[r][k] = w;
+    for (int k = k0; on && k < c.parts; k += lanes) m = fmaxf(m, __ldcg(mz_of + slot(k) * slot_rows + r).x);
+    for (int o = lanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int k = k0; on && k < c.parts; k += lanes) {
+      const float2 mz = __ldcg(mz_of + slot(k) * slot_rows + r);
+      const float w = pj_weight(mz, m);
+      s_w[r * pitch + k] = w;
       if (w != 0.f) z += w * mz.y;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    if (lane == 0) {
+    for (int o = lanes / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    if (on && k0 == 0) {
       s_inv[r] = z == 0.f ? 0.f : 1.f / z;
       const int tok = (c.r0 + first + r) / g.G, hq = c.h * g.G + (c.r0 + first + r) - tok * g.G;
       if (g.lse)
@@ -71,48 +95,55 @@ __global__ void __launch_bounds__(kPjThreads) pg_join_kernel(PjArgs a) {
     }
   }
   __syncthreads();
-  const int items = live * (DH / 4), pass = min(items, kPjThreads), groups = kPjThreads / pass;
+  if (!few) {
+    // numerators [column / 4][row]: four of a thread at a time
+    constexpr int kPer = kPjRows * kC4 / kPjThreads;
+    const int r = threadIdx.x % kPjRows, q0 = threadIdx.x / kPjRows;
+    if (r >= live) return;
+    const float4* n = a.tile_n + (size_t)q0 * kPgTileRows + first + r;
+    float4 acc[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int k = 0; k < c.parts; ++k) {
+      const float4* nk = n + slot(k) * kC4 * kPgTileRows;
+      float4 x[kPer];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) x[e] = __ldcg(nk + (size_t)e * (kPjThreads / kPjRows) * kPgTileRows);
+      const float w = s_w[r * pitch + k];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) pj_axpy(acc[e], w, x[e]);
+    }
+    const float inv = s_inv[r];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) pj_put<BF>(g, c, first + r, q0 + e * (kPjThreads / kPjRows), acc[e], inv);
+    return;
+  }
+  // numerators [row][column / 4]: as many groups of threads as the rows leave share the parts
+  const int items = live * kC4, pass = min(items, kPjThreads), groups = kPjThreads / pass;
   const int group = threadIdx.x / pass;
   for (int base = 0; base < items; base += pass) {
-    const int i = base + threadIdx.x - group * pass;
+    const int i = base + threadIdx.x - group * pass, r = i / kC4, c4 = i % kC4;
+    const bool on = group < groups && i < items;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    // the tile kernel's numerators lie [column / 4][row], the few-row kernel's [row][column / 4]
-    const int r = few ? i / (DH / 4) : i % live, c4 = few ? i % (DH / 4) : i / live;
-    if (group < groups && i < items) {
+    if (on) {
       const int k1 = c.parts * (group + 1) / groups;
 #pragma unroll 8
-      for (int k = c.parts * group / groups; k < k1; ++k) {
-        const float4 x = __ldcg(n_of + (few ? (slot(k) * kPgFewRows + r) * (DH / 4) + c4
-                                            : (slot(k) * (DH / 4) + c4) * kPgTileRows + first + r));
-        const float w = s_w[r][k];
-        if (w == 0.f) continue;
-        acc.x += w * x.x;
-        acc.y += w * x.y;
-        acc.z += w * x.z;
-        acc.w += w * x.w;
-      }
+      for (int k = c.parts * group / groups; k < k1; ++k)
+        pj_axpy(acc, s_w[r * pitch + k], __ldcg(a.row_n + (slot(k) * kPgFewRows + r) * kC4 + c4));
     }
     s_acc[threadIdx.x] = acc;
     __syncthreads();
-    if (group == 0 && i < items) {
-      for (int k = 1; k < groups; ++k) {
-        const float4 x = s_acc[k * pass + threadIdx.x];
-        acc.x += x.x;
-        acc.y += x.y;
-        acc.z += x.z;
-        acc.w += x.w;
-      }
-      const int tok = (c.r0 + first + r) / g.G, hq = c.h * g.G + (c.r0 + first + r) - tok * g.G;
-      const float inv = s_inv[r];
-      *reinterpret_cast<uint2*>(g.o.p + (c.q0 + tok) * g.o.st + hq * g.o.sh + c4 * 4) =
-          make_uint2(pg_pack2<BF>(acc.x * inv, acc.y * inv), pg_pack2<BF>(acc.z * inv, acc.w * inv));
+    if (on && group == 0) {
+      for (int k = 1; k < groups; ++k) pj_axpy(acc, 1.f, s_acc[k * pass + threadIdx.x]);
+      pj_put<BF>(g, c, r, c4, acc, s_inv[r]);
     }
     __syncthreads();
   }
 }
 
 int launch_pg_join(const PgArgs& g, int dh, int bf16, const PgScratch& ws, bool tiles, cudaStream_t stream) {
-  PjArgs a{g, ws.tile_cuts, ws.row_cuts, ws.tile_mz, ws.row_mz, ws.tile_n, ws.row_n, ws.row_cuts ? 2 * kPgSms : 0};
+  PjArgs a{g, ws.tile_cuts, ws.row_cuts, ws.row_cuts ? 2 * kPgSms : 0, ws.tile_mz, ws.row_mz, ws.tile_n, ws.row_n};
   const int blocks = a.row_blocks + (tiles ? kPgSms * (kPgTileRows / kPjRows) : 0);
   if (blocks == 0) return FLASHLOOP_OK;
   auto go = [&](auto kernel) { return pg_launch_early(kernel, dim3(blocks), kPjThreads, 0, stream, a); };

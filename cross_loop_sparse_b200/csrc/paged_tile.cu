@@ -708,21 +708,27 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       const bool live = r < it.n * g.G;
       const int tok = r / g.G, hq = it.h * g.G + r - tok * g.G;
       // write-back; a numerator is read once for all rows of the warp, whether live or not
+      const float inv = z == 0.f ? 0.f : 1.f / z;
       uint16_t* od = g.o.p + (live ? (it.q0 + tok) * g.o.st + (long long)hq * g.o.sh : 0);
-      auto put = [&](int cc, const float (&v)[32], float inv) {
+      auto put = [&](int cc, const float (&v)[32]) {
         if (!live) return;
+        uint32_t w[16];
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-          *reinterpret_cast<uint4*>(od + cc + 8 * w) =
-              make_uint4(pg_pack2<BF>(v[8 * w] * inv, v[8 * w + 1] * inv), pg_pack2<BF>(v[8 * w + 2] * inv, v[8 * w + 3] * inv),
-                         pg_pack2<BF>(v[8 * w + 4] * inv, v[8 * w + 5] * inv), pg_pack2<BF>(v[8 * w + 6] * inv, v[8 * w + 7] * inv));
+        for (int e = 0; e < 16; ++e) w[e] = pg_pack2<BF>(v[2 * e] * inv, v[2 * e + 1] * inv);
+        if (g.o32) {
+          st_global_v8(od + cc, *reinterpret_cast<uint32_t(*)[8]>(&w[0]));
+          st_global_v8(od + cc + 16, *reinterpret_cast<uint32_t(*)[8]>(&w[8]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(od + cc + 8 * e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        }
       };
       auto put_lse = [&](float m, float zz) {
         if (live && g.lse)
           g.lse[(size_t)hq * g.max_tokens + it.q0 + tok] = zz == 0.f ? -INFINITY : (m + log2f(zz)) * kPgLn2;
       };
       const size_t prow = (size_t)it.slot * kPtPair + x * kPtRows + row;
-      const float inv = z == 0.f ? 0.f : 1.f / z;
 #pragma unroll 1
       for (int cc = 0; cc < DH; cc += 32) {
         uint32_t w[32];
@@ -734,7 +740,7 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = my > 0 ? __uint_as_float(w[e]) : 0.f;
         if (it.parts == 1) {
-          put(cc, v, inv);
+          put(cc, v);
         } else if (live && my > 0) {
           float4* d = a.part_n + ((size_t)it.slot * (DH / 4) + cc / 4) * kPtPair + x * kPtRows + row;
 #pragma unroll
