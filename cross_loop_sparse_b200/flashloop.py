@@ -380,7 +380,7 @@ def _rows(fn, name, t, shape, dtype, dev, written=False):
     st, sh, se = t.stride()
     if se != 1:
         raise FlashLoopError(fn, -1, f"{name}: head_dim has to be contiguous")
-    if written and not (st or shape[0] < 2) or written and not (sh or shape[1] < 2):
+    if written and (st == 0 and shape[0] > 1 or sh == 0 and shape[1] > 1):
         raise FlashLoopError(fn, -1, f"{name}: rows that overlap")
     return RowsC(t.data_ptr(), st, sh)
 
@@ -393,7 +393,7 @@ def _pages(fn, name, t, p, dtype, dev, written=False):
     sp, st, sh, se = t.stride()
     if se != 1:
         raise FlashLoopError(fn, -1, f"{name}: head_dim has to be contiguous")
-    if written and not all(x or n < 2 for x, n in zip((sp, st, sh), shape)):
+    if written and (sp == 0 and shape[0] > 1 or st == 0 or sh == 0 and shape[2] > 1):
         raise FlashLoopError(fn, -1, f"{name}: pages that overlap")
     return PagesC(t.data_ptr(), sp, st, sh)
 

@@ -342,3 +342,305 @@ def test_paged_attention_reports_bad_pages_and_lengths(new):
         F.flashloop_paged_attn(p, q, kc, vc, table, ints(lens), ints(c), o, None, ws, err)
         assert err.item() == 2 and (o[:new] != 7).any() and not (o[:new] == 7).all(2).any()
         assert c is not cu or (o[new:2 * new] == 7).all()
+
+
+# ------------------------------------------------------------------------------- many shapes
+def random_paged(seed):
+    rng = random.Random(seed)
+    Hk, G = rng.choice((1, 2, 3, 8)), rng.choice((1, 2, 3, 4, 5, 8, 16, 33))
+    dh, page = rng.choice((64, 128)), rng.choice((16, 32, 64, 128, 256))
+    B = rng.choice((1, 2, 5, 33, 70, 140))
+    big = max(1, 6000 // (B * G * Hk))
+    new = [rng.choice((0, 1, 1, 1, rng.randint(1, 4), rng.randint(1, 60 if B > 5 else 600))) for _ in range(B)]
+    new = [min(n, big * 8) for n in new]
+    total = [max(0, n + rng.choice((0, 0, rng.randint(0, 300), rng.randint(0, 3000 if B < 40 else 400), -rng.randint(0, 3)))) for n in new]
+    return total, new, Hk * G, Hk, dh, page, rng.choice((BF, HF)), rng.choice(("thd", "htd", "both")), rng.choice((0, 3))
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_paged_attention_over_random_batches(seed):
+    total, new, H, Hk, dh, page, dt, layout, pad = random_paged(seed)
+    p, q, kc, vc, table, cu = paged_inputs(total, new, H, Hk, dh, page, dt, layout, pad, seed)
+    o, lse, err, ws = torch.full_like(q, 7.0), torch.full((H, q.shape[0]), 7.0, device="cuda"), ints([0]), workspace(p)
+    F.flashloop_paged_attn(p, q, kc, vc, table, ints(total), ints(cu), o, lse, ws, err)
+    refs = [attention(q[cu[b]:cu[b + 1]], gather(kc, table[b], t), gather(vc, table[b], t), t - new[b], dh ** -0.5) for b, t in enumerate(total)]
+    check(o, lse, cu, refs, True)
+    assert err.item() == 0
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_prompt_attention_over_random_batches(seed):
+    rng = random.Random(1000 + seed)
+    Hk, G, dh, dt = rng.choice((1, 2, 5)), rng.choice((1, 2, 3, 7, 8)), rng.choice((64, 128)), rng.choice((BF, HF))
+    B = rng.choice((1, 3, 40, 130))
+    lens = [rng.choice((0, 1, rng.randint(1, 100), rng.randint(1, 1500 if B < 4 else 300))) for _ in range(B)]
+    g, cu, H = gen(seed), starts(lens), Hk * G
+    T = max(1, cu[-1] + rng.choice((0, 9)))
+    q, k, v = randn(g, T, H, dh, dtype=dt, std=2.0), randn(g, T, Hk, dh, dtype=dt), randn(g, T, Hk, dh, dtype=dt)
+    o, lse, err = torch.full_like(q, 7.0), torch.full((H, T), 7.0, device="cuda"), ints([0])
+    p = F.PagedParams.make(batch=B, max_tokens=T, max_new=max(1, max(lens)), n_heads=H, n_kv_heads=Hk, head_dim=dh, dtype=dt, scale=0.3)
+    F.flashloop_prompt_attn(p, q, k, v, ints(cu), o, lse, err)
+    check(o, lse, cu, [attention(q[a:b], k[a:b], v[a:b], 0, 0.3) for a, b in zip(cu, cu[1:])], True)
+    assert err.item() == 0
+
+
+def test_peaked_and_shifted_scores():
+    """Scores hundreds apart, rising along the columns (the running reference is raised again and again), and far from zero."""
+    g, n, dh = gen(9), 700, 128
+    for rise in (1.0, -1.0):
+        q = torch.ones(n, 2, dh, device="cuda").to(BF)
+        k = (torch.arange(n, device="cuda")[:, None, None] * rise * 0.05 + randn(g, n, 1, dh)).to(BF)
+        v = randn(g, n, 1, dh, dtype=BF)
+        p = F.PagedParams.make(batch=1, max_tokens=n, max_new=n, n_heads=2, n_kv_heads=1, head_dim=dh)
+        o, lse, err = torch.empty(n, 2, dh, dtype=BF, device="cuda"), torch.empty(2, n, device="cuda"), ints([0])
+        F.flashloop_prompt_attn(p, q, k, v, ints([0, n]), o, lse, err)
+        check(o, lse, [0, n], [attention(q, k, v, 0, dh ** -0.5)], True)
+
+
+def test_equal_keys_average_the_values():
+    n, dh = 300, 64
+    q, k = torch.ones(n, 1, dh, dtype=HF, device="cuda"), torch.ones(n, 1, dh, dtype=HF, device="cuda")
+    v = torch.full((n, 1, dh), 0.5, dtype=HF, device="cuda")
+    p = F.PagedParams.make(batch=1, max_tokens=n, max_new=n, n_heads=1, n_kv_heads=1, head_dim=dh, dtype=HF)
+    o, lse = torch.empty_like(q), torch.empty(1, n, device="cuda")
+    F.flashloop_prompt_attn(p, q, k, v, ints([0, n]), o, lse, ints([0]))
+    assert (o == 0.5).all()
+    want = math.sqrt(dh) + torch.log(torch.arange(1, n + 1, device="cuda", dtype=torch.float64))
+    assert ((lse[0].double() - want).abs() <= 2.0 ** -20 * want).all()
+
+
+# ------------------------------------------------------------------------------- layouts, streams, graphs
+def test_broadcast_keys_and_odd_alignment():
+    """Key heads that are one head expanded, rows of o on 16 bytes only, queries transposed."""
+    g, T, H, dh = gen(3), 260, 4, 128
+    k1, v1 = randn(g, T, 1, dh, dtype=BF), randn(g, T, 1, dh, dtype=BF)
+    k, v = k1.expand(T, 2, dh), v1.expand(T, 2, dh)
+    q = randn(g, H, T, dh, dtype=BF).transpose(0, 1)
+    wide = torch.full((T, H, dh + 8), 7.0, dtype=BF, device="cuda")
+    o, err = wide[:, :, 8:], ints([0])
+    p = F.PagedParams.make(batch=1, max_tokens=T, max_new=T, n_heads=H, n_kv_heads=2, head_dim=dh)
+    F.flashloop_prompt_attn(p, q, k, v, ints([0, T]), o, None, err)
+    ref = attention(q, k, v, 0, dh ** -0.5)
+    assert ((o.double() - ref[0]).abs() <= ref[2]).all() and (wide[:, :, :8] == 7).all()
+    o2 = torch.full((T, H, dh + 8), 7.0, dtype=BF, device="cuda")
+    F.flashloop_prompt_attn(p, q, k.contiguous(), v.contiguous(), ints([0, T]), o2[:, :, 8:], None, err)
+    assert ((o2[:, :, 8:].double() - ref[0]).abs() <= ref[2]).all() and (o2[:, :, :8] == 7).all()
+    for new in (1, T):  # over a cache whose pages are one page expanded
+        kc = k1[:64].view(1, 64, 1, dh).expand(4, 64, 2, dh)
+        vc = v1[:64].view(1, 64, 1, dh).expand(4, 64, 2, dh)
+        pp = F.PagedParams.make(batch=1, max_tokens=new, max_new=new, n_heads=H, n_kv_heads=2, head_dim=dh, page_size=64, n_pages=4, max_blocks=5)
+        oo, table = torch.empty(new, H, dh, dtype=BF, device="cuda"), ints([[3, 1, 2, 0, 0]])
+        F.flashloop_paged_attn(pp, q[:new], kc, vc, table, ints([T]), ints([0, new]), oo, None, workspace(pp), err)
+        ref = attention(q[:new], gather(kc, table[0], T), gather(vc, table[0], T), T - new, dh ** -0.5)
+        assert ((oo.double() - ref[0]).abs() <= ref[2]).all()
+    assert err.item() == 0
+
+
+def test_offsets_beyond_32_bits():
+    """A pool of more than 2^31 elements a cache; the requests' pages lie at both ends."""
+    page, Hk, dh, H = 64, 4, 128, 8
+    n_pages = (1 << 31) // (page * Hk * dh) + 900
+    kc = torch.empty(n_pages, page, Hk, dh, dtype=BF, device="cuda")
+    vc = torch.empty(n_pages, page, Hk, dh, dtype=BF, device="cuda")
+    table = ints([list(range(n_pages - 12, n_pages)), list(range(12))])
+    g, total = gen(4), [750, 700]
+    slots = torch.cat([table[b].long()[torch.arange(t, device="cuda") // page] * page + torch.arange(t, device="cuda") % page for b, t in enumerate(total)])
+    k, v = randn(g, sum(total), Hk, dh, dtype=BF), randn(g, sum(total), Hk, dh, dtype=BF)
+    err = ints([0])
+    p = F.PagedParams.make(batch=2, max_tokens=sum(total), max_new=750, n_heads=H, n_kv_heads=Hk, head_dim=dh, page_size=page, n_pages=n_pages, max_blocks=12)
+    F.flashloop_paged_kv_write(p, k, v, slots.to(torch.int32), kc, vc, err)
+    assert torch.equal(gather(kc, table[0], 750), k[:750]) and torch.equal(gather(vc, table[1], 700), v[750:])
+    for new in ([1, 1], [300, 50]):
+        cu = starts(new)
+        p = F.PagedParams.make(batch=2, max_tokens=cu[-1], max_new=max(new), n_heads=H, n_kv_heads=Hk, head_dim=dh, page_size=page, n_pages=n_pages, max_blocks=12)
+        q = randn(g, cu[-1], H, dh, dtype=BF)
+        o = torch.empty_like(q)
+        F.flashloop_paged_attn(p, q, kc, vc, table, ints(total), ints(cu), o, None, workspace(p), err)
+        for b, (a, z) in enumerate(((0, 750), (750, 1450))):
+            ref = attention(q[cu[b]:cu[b + 1]], k[a:z], v[a:z], total[b] - new[b], dh ** -0.5)
+            assert ((o[cu[b]:cu[b + 1]].double() - ref[0]).abs() <= ref[2]).all()
+    assert err.item() == 0
+
+
+def test_two_streams_at_once_and_a_shared_workspace_in_turn():
+    a = paged_inputs([3000, 900, 70], [1, 200, 9], 8, 2, 128, 64, BF, "thd", 0, seed=1)
+    b = paged_inputs([12000, 40, 5000], [1, 1, 1], 16, 2, 64, 16, HF, "thd", 0, seed=2)
+    lens = (ints([3000, 900, 70]), ints([12000, 40, 5000]))
+    ws = [workspace(a[0]), workspace(b[0])]
+    both = torch.empty(max(w.numel() for w in ws), dtype=torch.uint8, device="cuda")
+    err = ints([0])
+
+    def run(x, kv, w, o):
+        p, q, kc, vc, table, cu = x
+        F.flashloop_paged_attn(p, q, kc, vc, table, kv, ints(cu) if not isinstance(cu, torch.Tensor) else cu, o, None, w, err)
+
+    a, b = a[:5] + (ints(a[5]),), b[:5] + (ints(b[5]),)
+    want = [torch.empty_like(a[1]), torch.empty_like(b[1])]
+    run(a, lens[0], ws[0], want[0])
+    run(b, lens[1], ws[1], want[1])
+    torch.cuda.synchronize()
+    got = [torch.zeros_like(a[1]), torch.zeros_like(b[1])]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):  # two calls at once, each with a workspace of its own
+        for s, x, kv, w, o in zip(streams, (a, b), lens, ws, got):
+            with torch.cuda.stream(s):
+                run(x, kv, w, o)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # two captured graphs that share a workspace, replayed in turn
+    graphs = []
+    for x, kv, o in zip((a, b), lens, got):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(x, kv, both, o)
+        graphs.append(g)
+    for o in got:
+        o.zero_()
+    both.fill_(0xFF)
+    for i in range(6):
+        graphs[i % 2].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and err.item() == 0
+
+
+class Served:
+    """Requests served from one pool: plan, write, attention, as a captured step or eagerly."""
+
+    def __init__(self, B, T, max_new, H, Hk, dh, page, n_pages, width, dt=BF):
+        self.p = F.PagedParams.make(batch=B, max_tokens=T, max_new=max_new, n_heads=H, n_kv_heads=Hk, head_dim=dh, page_size=page, n_pages=n_pages,
+                                    max_blocks=width, dtype=dt)
+        self.kv, self.kv_out, self.new = ints([0] * B), ints([0] * B), ints([0] * B)
+        self.free, self.n_free, self.n_out = ints(list(range(n_pages))), ints([n_pages]), ints([0])
+        self.table, self.cu = torch.full((B, width), -1, dtype=torch.int32, device="cuda"), ints([0] * (B + 1))
+        self.slots, self.pos, self.err = ints([0] * T), ints([0] * T), ints([0])
+        self.kc, self.vc = (torch.full((n_pages, page, Hk, dh), math.nan, dtype=dt, device="cuda") for _ in range(2))
+        self.q, self.k, self.v = (torch.zeros(T, h, dh, dtype=t, device="cuda") for h, t in ((H, dt), (Hk, torch.float32), (Hk, torch.float32)))
+        self.o, self.ws = torch.zeros(T, H, dh, dtype=dt, device="cuda"), workspace(self.p)
+
+    def step(self):
+        F.flashloop_paged_plan(self.p, self.kv, self.new, self.free, self.n_free, self.table, self.cu, self.kv_out, self.slots, self.pos, self.n_out, self.err)
+        F.flashloop_paged_kv_write(self.p, self.k, self.v, self.slots, self.kc, self.vc, self.err)
+        F.flashloop_paged_attn(self.p, self.q, self.kc, self.vc, self.table, self.kv_out, self.cu, self.o, None, self.ws, self.err)
+        self.kv.copy_(self.kv_out)
+        self.n_free.copy_(self.n_out)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_serving_steps_of_changing_lengths(captured):
+    """Chunks, then single tokens, requests joining late: each step's rows attend to all that was written before."""
+    H, Hk, dh, page = 8, 2, 64, 16
+    s = Served(B=4, T=320, max_new=200, H=H, Hk=Hk, dh=dh, page=page, n_pages=96, width=32)
+    g, hist = gen(11), [[[], []] for _ in range(4)]
+    if captured:
+        s.step()  # no new tokens
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            s.step()
+    for new in ([100, 0, 33, 0], [100, 7, 1, 0], [1, 1, 1, 200], [1, 0, 1, 100], [1, 1, 1, 1], [1, 1, 1, 1], [0, 0, 0, 0], [16, 200, 16, 1]):
+        n = sum(new)
+        s.new.copy_(ints(new))
+        s.q.copy_(randn(g, 320, H, dh, dtype=BF))
+        s.k.copy_(randn(g, 320, Hk, dh))
+        s.v.copy_(randn(g, 320, Hk, dh))
+        s.o.fill_(7.0)
+        graph.replay() if captured else s.step()
+        cu = starts(new)
+        assert s.cu.tolist() == cu and s.err.item() == 0 and (s.o[n:] == 7).all()
+        for b in range(4):
+            r = slice(cu[b], cu[b + 1])
+            hist[b][0].append(s.k[r].to(BF).clone())
+            hist[b][1].append(s.v[r].to(BF).clone())
+            k, v = torch.cat(hist[b][0]), torch.cat(hist[b][1])
+            assert s.kv[b].item() == k.shape[0] and s.pos[r].tolist() == list(range(k.shape[0] - new[b], k.shape[0]))
+            o, _, tol, _ = attention(s.q[r], k, v, k.shape[0] - new[b], dh ** -0.5)
+            assert ((s.o[r].double() - o).abs() <= tol).all()
+    held = {x for b in range(4) for x in s.table[b, :-(-s.kv[b].item() // page)].tolist()}
+    assert len(held) == sum(-(-n // page) for n in s.kv.tolist()) and s.n_free.item() == 96 - len(held)
+    assert not held & set(s.free[:s.n_free.item()].tolist())
+
+
+def test_with_the_projections_of_the_sublayer():
+    """Projection with RoPE at the planned positions, cache write, attention and output projection,
+    for two requests in two chunks each and then a token each."""
+    from workload import CONFIGS, make_weights
+    from gpu_helpers import bf16_to_torch
+    cfg = CONFIGS["tiny"]
+    d, H, dh = cfg.d_model, cfg.n_heads, cfg.head_dim
+    W = make_weights(cfg)
+    wqkv, wo = bf16_to_torch(W["wqkv"]), bf16_to_torch(W["wo"])
+    params = F.Params.from_config(cfg)
+    rope = torch.zeros(256, dh // 2, 2, device="cuda")
+    F.flashloop_rope_table(params, 256, rope)
+    s = Served(B=2, T=256, max_new=120, H=H, Hk=H, dh=dh, page=32, n_pages=16, width=8)
+    g = gen(21)
+    x = [randn(g, n, d, dtype=BF) for n in (200, 90)]
+    y, done = [[], []], [0, 0]
+    for new in ([120, 50], [79, 39], [1, 1]):
+        n = sum(new)
+        rows = torch.zeros(256, d, dtype=BF, device="cuda")
+        rows[:n] = torch.cat([x[b][done[b]:done[b] + new[b]] for b in range(2)])
+        s.new.copy_(ints(new))
+        F.flashloop_paged_plan(s.p, s.kv, s.new, s.free, s.n_free, s.table, s.cu, s.kv_out, s.slots, s.pos, s.n_out, s.err)
+        cs = rope[s.pos.long()].contiguous()
+        F.flashloop_qkv_gathered(params, rows, None, None, 256, wqkv, cs, s.q.view(256, d), s.k.view(256, d), s.v.view(256, d))
+        F.flashloop_paged_kv_write(s.p, s.k, s.v, s.slots, s.kc, s.vc, s.err)
+        F.flashloop_paged_attn(s.p, s.q, s.kc, s.vc, s.table, s.kv_out, s.cu, s.o, None, s.ws, s.err)
+        out = torch.zeros(256, d, dtype=BF, device="cuda")
+        F.flashloop_out_proj(params, s.o.view(256, d), None, None, 256, wo, out)
+        for b, (a, z) in enumerate(((0, new[0]), (new[0], n))):
+            y[b].append(out[a:z].clone())
+            done[b] += new[b]
+        s.kv.copy_(s.kv_out)
+        s.n_free.copy_(s.n_out)
+    assert s.err.item() == 0
+    w = wqkv.double()
+    ang = torch.arange(200, device="cuda", dtype=torch.float64)[:, None] * cfg.rope_theta ** (-torch.arange(dh // 2, device="cuda", dtype=torch.float64) * 2 / dh)
+    cos, sin = torch.cos(ang)[:, None], torch.sin(ang)[:, None]
+    for b, n in enumerate((200, 90)):
+        q, k, v = (x[b].double() @ w.T).view(n, 3, H, dh).unbind(1)
+
+        def turn(t):
+            lo, hi = t[..., :dh // 2], t[..., dh // 2:]
+            return torch.cat([lo * cos[:n] - hi * sin[:n], hi * cos[:n] + lo * sin[:n]], -1)
+        q, k = turn(q), turn(k)
+        a = torch.einsum("ihd,jhd->hij", q, k) / math.sqrt(dh)
+        a = a.masked_fill(torch.ones(n, n, device="cuda", dtype=torch.bool).triu(1), -math.inf).softmax(-1)
+        want = torch.einsum("hij,jhd->ihd", a, v).reshape(n, d) @ wo.double().T
+        got = torch.cat(y[b]).double()
+        # the sublayer's own bar: 1e-2 of a row's norm (q, K, V, P, O and Y are rounded to bf16)
+        assert (((got - want).norm(dim=1) / want.norm(dim=1)) < 1e-2).all()
+
+
+# ------------------------------------------------------------------------------- refusals on the device
+def test_binding_refusals():
+    g = gen(0)
+    p = F.PagedParams.make(batch=1, max_tokens=8, max_new=8, n_heads=2, n_kv_heads=1, head_dim=64, page_size=16, n_pages=2, max_blocks=2)
+    q, k = randn(g, 8, 2, 64, dtype=BF), randn(g, 8, 1, 64, dtype=BF)
+    o, cu, err, ws = torch.full_like(q, 7.0), ints([0, 8]), ints([0]), workspace(p)
+    kc = torch.zeros(2, 16, 1, 64, dtype=BF, device="cuda")
+    table, kv = ints([[0, 1]]), ints([8])
+    odd = torch.zeros(8 * 2 * 64 + 4, dtype=BF, device="cuda")[4:].view(8, 2, 64)
+    prompt = lambda **a: F.flashloop_prompt_attn(**{**dict(params=p, q=q, k=k, v=k, cu=cu, o=o, lse=None, err_word=err), **a})  # noqa: E731
+    paged = lambda **a: F.flashloop_paged_attn(**{**dict(params=p, q=q, k_cache=kc, v_cache=kc, block_table=table, kv_lens=kv, cu=cu, o=o, lse=None,  # noqa: E731
+                                                          workspace=ws, err_word=err), **a})
+    write = lambda **a: F.flashloop_paged_kv_write(**{**dict(params=p, k=k, v=k, slot_map=ints([0] * 8), k_cache=kc, v_cache=kc, err_word=err), **a})  # noqa: E731
+    bad = [
+        (prompt, dict(q=q.to(HF)), -1), (prompt, dict(q=q[:7]), -1), (prompt, dict(q=q.cpu()), -1), (prompt, dict(k=k.float()), -1), (prompt, dict(q=odd), -1),
+        (prompt, dict(o=odd), -1), (prompt, dict(q=q.transpose(1, 2).contiguous().transpose(1, 2)), -1), (prompt, dict(cu=cu.long()), -1), (prompt, dict(cu=cu[:1]), -1),
+        (prompt, dict(o=o[:1].expand(8, 2, 64)), -1), (prompt, dict(lse=torch.zeros(15, device="cuda")), -1), (prompt, dict(err_word=ints([0]).cpu()), -1),
+        (paged, dict(block_table=table[:, :1]), -1), (paged, dict(workspace=ws[:8]), -1), (paged, dict(workspace=torch.empty(64, dtype=torch.uint8, device="cuda")[8:]), -1),
+        (paged, dict(k_cache=kc[:1]), -1), (paged, dict(kv_lens=kv.cpu()), -1), (paged, dict(workspace=ws.cpu()), -1),
+        (write, dict(k=k.to(HF), v=k.to(HF)), -2), (write, dict(v=k.float()), -1), (write, dict(k_cache=kc[:1].expand(2, 16, 1, 64)), -1),
+        (write, dict(k=k.double(), v=k.double()), -2),
+    ]
+    for call, args, status in bad:
+        with pytest.raises(F.FlashLoopError) as e:
+            call(**args)
+        assert e.value.status == status, args.keys()
+    for field, value, status in (("head_dim", 96, -1), ("n_kv_heads", 3, -1), ("dtype", 2, -2), ("dtype", 7, -2)):
+        bad = F.PagedParams.from_buffer_copy(p)
+        setattr(bad, field, value)
+        with pytest.raises(F.FlashLoopError) as e:
+            prompt(params=bad)
+        assert e.value.status == status
+    assert (o == 7).all() and err.item() == 0
