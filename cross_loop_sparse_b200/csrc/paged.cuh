@@ -19,8 +19,24 @@ struct PgPages {  // 16-bit pages [page, token, head, head_dim]; packed rows are
   long long sp, st, sh;
 };
 
+// Division by the group, whose size is no constant: for 0 <= x < 2^31 and d > 1,
+// x / d = (x * mul) >> (32 + shift) with mul = ceil(2^(32 + shift) / d) and
+// 2^(shift + 1) >= d, since the error of mul adds less than x / 2^31 <= 1 / d steps.
+struct PgDiv {
+  uint32_t mul;  // 0: d is 1
+  int shift;
+  __device__ __forceinline__ int operator()(int x) const { return mul ? (int)(__umulhi((uint32_t)x, mul) >> shift) : x; }
+};
+inline PgDiv pg_divide_by(int d) {
+  if (d <= 1) return {0, 0};
+  int log = 0;
+  while ((1ll << log) < d) ++log;
+  return {(uint32_t)(((1ull << (31 + log)) + d - 1) / d), log - 1};
+}
+
 struct PgArgs {
   int B, Hq, Hk, G, max_tokens, max_new;
+  PgDiv by_g;                      // x / G
   int shift, n_pages, max_blocks;  // page_size = 1 << shift
   const int32_t* table;            // NULL: keys and values are packed rows
   const int32_t* kv_lens;          // NULL: a request's cached length is its number of rows
@@ -31,7 +47,6 @@ struct PgArgs {
   int32_t* err;
   float scale_log2;  // scale * log2(e) > 0: scores in log2 units
   int o32;           // rows of o begin on 32 bytes: whole sectors are written
-  int skip_longer;   // requests with more than max_new rows are another kernel's, not a fault
 };
 
 // Request b: rows [q0, q0 + n) and L columns; n = 0 for one that the call
@@ -45,13 +60,12 @@ __device__ __forceinline__ PgSeq pg_seq(const PgArgs& g, int b) {
   s.q0 = c0;
   s.n = c1 - c0;
   s.L = g.kv_lens ? g.kv_lens[b] : s.n;
-  bool bad = c0 < 0 || c1 < c0 || c1 > g.max_tokens || (s.n > g.max_new && !g.skip_longer) || s.L < 0;
+  bool bad = c0 < 0 || c1 < c0 || c1 > g.max_tokens || s.n > g.max_new || s.L < 0;
   if (g.table) bad = bad || (long long)s.L > ((long long)g.max_blocks << g.shift);
   if (bad) {
     set_error(g.err, FLASHLOOP_DEVERR_INDEX);
     s.q0 = s.n = s.L = 0;
   }
-  if (g.skip_longer && s.n > g.max_new) s.n = 0;
   return s;
 }
 
@@ -96,10 +110,8 @@ struct PgScratch {
   size_t total;
 };
 
-// The kernels of one call overlap: a later one is launched when all blocks of
-// the one before have started, and waits for its end only where it reads what
-// that wrote.  A kernel that needs nothing of the one before still waits at
-// its end, so that its own end means that everything before has ended.
+// The join overlaps the kernel before it: it is launched when all that one's
+// blocks have started, and waits for its end.
 __device__ __forceinline__ void pg_launch_next() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 __device__ __forceinline__ void pg_wait_for_launch_before() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 template <typename Kernel, typename... Args>
@@ -117,8 +129,12 @@ inline int pg_launch_early(Kernel kernel, dim3 grid, int threads, size_t smem, c
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? FLASHLOOP_OK : FLASHLOOP_ERR_CUDA;
 }
 
-// Requests of at most this many packed rows (rows x group) are the few-row
-// kernel's, which reads the cache once for 32 of them; longer ones the tile kernel's.
+// A call whose requests have at most this many packed rows (max_new x group) is
+// the few-row kernel's, any other the tile kernel's, whole: short requests among
+// long ones cost a tile kernel's block no more than HBM takes to bring their keys
+// and values (3000 cycles a 128-column tile against 2700), while a second kernel
+// for them comes on top: 255 us against 248 us for 32 decoding requests beside two
+// chunks of 1500 rows, and a launch that does nothing where none decodes.
 constexpr int kPgFewRows = 32;
 
 // Tables of at most this many columns are not cut: whole requests are a few
@@ -126,8 +142,7 @@ constexpr int kPgFewRows = 32;
 constexpr int kPgShort = 512;
 
 int launch_pg_rows(const PgArgs& g, int dh, int bf16, const PgScratch& ws, cudaStream_t stream);
-// early: behind the few-row kernel of the same call
-int launch_pg_tile(const PgArgs& g, int dh, int bf16, int few, const PgScratch& ws, bool early, cudaStream_t stream);
-int launch_pg_join(const PgArgs& g, int dh, int bf16, const PgScratch& ws, bool tiles, cudaStream_t stream);
+int launch_pg_tile(const PgArgs& g, int dh, int bf16, const PgScratch& ws, cudaStream_t stream);
+int launch_pg_join(const PgArgs& g, int dh, int bf16, const PgScratch& ws, cudaStream_t stream);
 
 }  // namespace fl

@@ -77,6 +77,11 @@ static bool pg_tma_ok(const PgArgs& g, int pages) {
   return true;
 }
 
+static bool pg_tiles(const flashloop_paged_params* p) {
+  const long long most = p->max_new < p->max_tokens ? p->max_new : p->max_tokens;
+  return most * (p->n_heads / p->n_kv_heads) > kPgFewRows;
+}
+
 // Offsets depend on the shape alone.
 static PgScratch pg_scratch(const flashloop_paged_params* p, void* base) {
   PgScratch w{};
@@ -87,12 +92,11 @@ static PgScratch pg_scratch(const flashloop_paged_params* p, void* base) {
     return at;
   };
   const size_t slots = 2 * kPgSms, row_slots = 4 * kPgSms, dh = (size_t)p->head_dim;
-  if ((long long)p->max_new * (p->n_heads / p->n_kv_heads) > kPgFewRows) {
+  if (pg_tiles(p)) {
     w.tile_cuts = ws_ptr<PgCut>(base, take(kPgSms * sizeof(PgCut)));
     w.tile_mz = ws_ptr<float2>(base, take(slots * kPgTileRows * sizeof(float2)));
     w.tile_n = ws_ptr<float4>(base, take(slots * kPgTileRows * dh * sizeof(float)));
-  }
-  if ((long long)p->max_blocks * p->page_size > kPgShort) {
+  } else if ((long long)p->max_blocks * p->page_size > kPgShort) {
     w.row_cuts = ws_ptr<PgCut>(base, take(2 * kPgSms * sizeof(PgCut)));
     w.row_mz = ws_ptr<float2>(base, take(row_slots * kPgFewRows * sizeof(float2)));
     w.row_n = ws_ptr<float4>(base, take(row_slots * kPgFewRows * dh * sizeof(float)));
@@ -108,6 +112,7 @@ static PgArgs pg_args(const flashloop_paged_params* p, const flashloop_rows* q, 
   g.Hq = p->n_heads;
   g.Hk = p->n_kv_heads;
   g.G = p->n_heads / p->n_kv_heads;
+  g.by_g = pg_divide_by(g.G);
   g.max_tokens = p->max_tokens;
   g.max_new = p->max_new < p->max_tokens ? p->max_new : p->max_tokens;
   g.cu = cu;
@@ -183,7 +188,7 @@ int flashloop_prompt_attn(const flashloop_paged_params* p, const flashloop_rows*
   const int bf16 = p->dtype == FLASHLOOP_DTYPE_BF16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!pg_tma_ok(g, 1)) return launch_pg_rows(g, p->head_dim, bf16, PgScratch{}, s);
-  return launch_pg_tile(g, p->head_dim, bf16, 0, PgScratch{}, false, s);
+  return launch_pg_tile(g, p->head_dim, bf16, PgScratch{}, s);
 }
 
 size_t flashloop_paged_attn_workspace_bytes(const flashloop_paged_params* p) {
@@ -221,19 +226,9 @@ int flashloop_paged_attn(const flashloop_paged_params* p, const flashloop_rows* 
   const int bf16 = p->dtype == FLASHLOOP_DTYPE_BF16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const PgScratch ws = pg_scratch(p, workspace);
-  if ((long long)g.max_new * g.G <= kPgFewRows) {
-    rc = launch_pg_rows(g, p->head_dim, bf16, ws, s);
-    return rc != FLASHLOOP_OK ? rc : launch_pg_join(g, p->head_dim, bf16, ws, false, s);
-  }
-  if (!pg_tma_ok(g, p->n_pages)) return launch_pg_rows(g, p->head_dim, bf16, PgScratch{}, s);
-  PgArgs few = g;
-  few.max_new = kPgFewRows / g.G;
-  few.skip_longer = 1;
-  PgScratch rows_ws = ws;
-  if (few.max_new > 0) rc = launch_pg_rows(few, p->head_dim, bf16, ws, s);
-  else rows_ws.row_cuts = nullptr;  // no request has so few packed rows
-  if (rc == FLASHLOOP_OK) rc = launch_pg_tile(g, p->head_dim, bf16, kPgFewRows, ws, few.max_new > 0, s);
-  return rc != FLASHLOOP_OK ? rc : launch_pg_join(g, p->head_dim, bf16, rows_ws, true, s);
+  if (pg_tiles(p) && !pg_tma_ok(g, p->n_pages)) return launch_pg_rows(g, p->head_dim, bf16, PgScratch{}, s);
+  rc = pg_tiles(p) ? launch_pg_tile(g, p->head_dim, bf16, ws, s) : launch_pg_rows(g, p->head_dim, bf16, ws, s);
+  return rc != FLASHLOOP_OK ? rc : launch_pg_join(g, p->head_dim, bf16, ws, s);
 }
 
 }  // extern "C"

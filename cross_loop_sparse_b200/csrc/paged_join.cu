@@ -35,7 +35,7 @@ __device__ __forceinline__ float pj_weight(const float2& mz, float m) {
 
 template <int BF>
 __device__ __forceinline__ void pj_put(const PgArgs& g, const PgCut& c, int r, int c4, const float4& acc, float inv) {
-  const int tok = (c.r0 + r) / g.G, hq = c.h * g.G + (c.r0 + r) - tok * g.G;
+  const int tok = g.by_g(c.r0 + r), hq = c.h * g.G + (c.r0 + r) - tok * g.G;
   *reinterpret_cast<uint2*>(g.o.p + (c.q0 + tok) * g.o.st + hq * g.o.sh + c4 * 4) =
       make_uint2(pg_pack2<BF>(acc.x * inv, acc.y * inv), pg_pack2<BF>(acc.z * inv, acc.w * inv));
 }
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kPjThreads) pg_join_kernel(PjArgs a) {
     for (int o = lanes / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     if (on && k0 == 0) {
       s_inv[r] = z == 0.f ? 0.f : 1.f / z;
-      const int tok = (c.r0 + first + r) / g.G, hq = c.h * g.G + (c.r0 + first + r) - tok * g.G;
+      const int tok = g.by_g(c.r0 + first + r), hq = c.h * g.G + (c.r0 + first + r) - tok * g.G;
       if (g.lse)
         g.lse[(size_t)hq * g.max_tokens + c.q0 + tok] = z == 0.f ? -INFINITY : (m + log2f(z)) * kPgLn2;
     }
@@ -142,9 +142,9 @@ __global__ void __launch_bounds__(kPjThreads) pg_join_kernel(PjArgs a) {
   }
 }
 
-int launch_pg_join(const PgArgs& g, int dh, int bf16, const PgScratch& ws, bool tiles, cudaStream_t stream) {
+int launch_pg_join(const PgArgs& g, int dh, int bf16, const PgScratch& ws, cudaStream_t stream) {
   PjArgs a{g, ws.tile_cuts, ws.row_cuts, ws.row_cuts ? 2 * kPgSms : 0, ws.tile_mz, ws.row_mz, ws.tile_n, ws.row_n};
-  const int blocks = a.row_blocks + (tiles ? kPgSms * (kPgTileRows / kPjRows) : 0);
+  const int blocks = a.row_blocks + (ws.tile_cuts ? kPgSms * (kPgTileRows / kPjRows) : 0);
   if (blocks == 0) return FLASHLOOP_OK;
   auto go = [&](auto kernel) { return pg_launch_early(kernel, dim3(blocks), kPjThreads, 0, stream, a); };
   if (dh == 128) return bf16 ? go(pg_join_kernel<128, 1>) : go(pg_join_kernel<128, 0>);

@@ -70,7 +70,7 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
   const int rows = s.n * g.G;
   const int shift = g.table ? g.shift : 31;
   const int off = s.L - s.n;                 // row i sees j <= off + i
-  const int free_cols = off + r0 / g.G + 1;  // columns that every row sees
+  const int free_cols = off + g.by_g(r0) + 1;  // columns that every row sees
   const int ncols = s.c1;
   uint8_t* ring = smem + warp * C::kWarpRing;
 
@@ -82,7 +82,7 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       const int r = r0 + mt * 16 + hf * 8 + (lane >> 2);
-      const int tok = r / g.G;
+      const int tok = g.by_g(r);
       lim[mt][hf] = r < rows ? off + tok : -1;
       const uint16_t* src = g.q.p + (s.q0 + (r < rows ? tok : 0)) * g.q.st +
                             (long long)(h * g.G + (r < rows ? r - tok * g.G : 0)) * g.q.sh + (lane & 3) * 2;
@@ -279,7 +279,7 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
       if (c == 0) __stcg(a.part_mz + at, make_float2(mm, zz));
       continue;
     }
-    const int tok = (r0 + r) / g.G, hq = h * g.G + (r0 + r) - tok * g.G;
+    const int tok = g.by_g(r0 + r), hq = h * g.G + (r0 + r) - tok * g.G;
     const float inv = zz == 0.f ? 0.f : 1.f / zz;
     *reinterpret_cast<uint2*>(g.o.p + (s.q0 + tok) * g.o.st + hq * g.o.sh + c) =
         make_uint2(pg_pack2<BF>(acc.x * inv, acc.y * inv), pg_pack2<BF>(acc.z * inv, acc.w * inv));
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PrArgs a) {
     const PgSeq q = pg_seq(g, blockIdx.z);
     const int rows = q.n * g.G, r0 = blockIdx.x * PrCfg<DH, MT>::kRows;
     if (r0 >= rows) return;
-    const int seen = q.L - q.n + (min(rows, r0 + PrCfg<DH, MT>::kRows) - 1) / g.G + 1;  // by the tile's last row
+    const int seen = q.L - q.n + g.by_g(min(rows, r0 + PrCfg<DH, MT>::kRows) - 1) + 1;  // by the tile's last row
     PrItem it{(int)blockIdx.z, (int)blockIdx.y, q.q0, q.n, q.L, r0, 0, max(0, seen), 0, 1};
     pr_item<DH, BF, MT>(a, it, smem);
     return;

@@ -65,7 +65,8 @@ constexpr int kPtWarpQ = 8, kPtWarpTma = 12, kPtWarpMma = 13, kPtWarpSched = 15;
 constexpr float kPtRescale = 8.f;
 constexpr int kPtRegsRows = 192, kPtRegsRest = 64;  // of the 65536 registers: 256 threads of each
 constexpr int kPtReaders = 15;   // arrivals that free a work item's slot: 8 + 4 + 1 + 2 warps
-constexpr int kPtMinUnits = 4;   // column tiles a block takes at least when the line is cut
+constexpr int kPtMinUnits = 4;   // units a block takes at least when the line is cut
+constexpr int kPtStart = 2;      // units of an item beside its column tiles: what starting and writing it costs
 
 template <int DH>
 struct PtCfg {
@@ -88,7 +89,6 @@ struct PtItem {
 
 struct PtArgs {
   PgArgs g;
-  int few;        // requests with at most this many packed rows are another kernel's
   int box_shift;  // tokens of a TMA box: 1 << box_shift
   PgCut* cuts;      // [grid]; NULL: items are whole
   float2* part_mz;  // [2 * grid, 256]
@@ -96,17 +96,16 @@ struct PtArgs {
 };
 
 __device__ __forceinline__ int pt_pairs(const PtArgs& a, int n) {
-  const int rows = n * a.g.G;
-  return rows <= a.few ? 0 : (rows + kPtPair - 1) / kPtPair;
+  return (n * a.g.G + kPtPair - 1) / kPtPair;
 }
 // Column tiles that the rows before packed row `end` see.
-__device__ __forceinline__ int pt_tiles(int n, int L, int G, int end) {
-  const int f = L - n + (min(end, n * G) - 1) / G + 1;
+__device__ __forceinline__ int pt_tiles(int n, int L, const PgArgs& g, int end) {
+  const int f = L - n + g.by_g(min(end, n * g.G) - 1) + 1;
   return f > 0 ? (f + kPtCols - 1) / kPtCols : 0;
 }
-// Column tiles of pair p; a pair that sees none still has its rows written.
-__device__ __forceinline__ int pt_units(int n, int L, int G, int p) {
-  return max(1, pt_tiles(n, L, G, (p + 1) * kPtPair));
+// Units of pair p on the line that is cut; a pair that sees no column still has its rows written.
+__device__ __forceinline__ int pt_units(int n, int L, const PgArgs& g, int p) {
+  return kPtStart + max(1, pt_tiles(n, L, g, (p + 1) * kPtPair));
 }
 
 // First of np pairs with at least `units` column tiles (they grow with the pair); np if none.
@@ -161,7 +160,7 @@ __device__ __forceinline__ void pt_schedule(const PtArgs& a, int lane, Emit emit
           it.n = __shfl_sync(kAll, s.n, src);
           it.L = __shfl_sync(kAll, s.L, src);
           it.r0 = (__shfl_sync(kAll, p1, src) - 1 - idx / g.Hk) * kPtPair;
-          it.t1 = pt_tiles(it.n, it.L, G, it.r0 + kPtPair);
+          it.t1 = pt_tiles(it.n, it.L, g, it.r0 + kPtPair);
           it.parts = 1;
           if (!emit(it)) return;
           ++round;
@@ -176,14 +175,14 @@ __device__ __forceinline__ void pt_schedule(const PtArgs& a, int lane, Emit emit
   auto head_units = [&]() -> long long {
     long long u = 0;
     if (np <= 8)
-      for (int p = 0; p < np; ++p) u += pt_units(s.n, s.L, G, p);
+      for (int p = 0; p < np; ++p) u += pt_units(s.n, s.L, g, p);
     unsigned big = __ballot_sync(kAll, np > 8);
     while (big) {
       const int src = __ffs(big) - 1;
       big &= big - 1;
       const int n_p = __shfl_sync(kAll, np, src), n = __shfl_sync(kAll, s.n, src), L = __shfl_sync(kAll, s.L, src);
       long long v = 0;
-      for (int p = lane; p < n_p; p += 32) v += pt_units(n, L, G, p);
+      for (int p = lane; p < n_p; p += 32) v += pt_units(n, L, g, p);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
       if (lane == src) u = v;
@@ -233,11 +232,11 @@ __device__ __forceinline__ void pt_schedule(const PtArgs& a, int lane, Emit emit
       // the pair that holds x: prefix sums over 32 pairs at a time
       for (int i0 = 0; i0 < n_p; i0 += 32) {
         const int i = i0 + lane;
-        const int u = i < n_p ? pt_units(it.n, it.L, G, n_p - 1 - i) : 0;
-        long long e = u;
+        const int u = i < n_p ? pt_units(it.n, it.L, g, n_p - 1 - i) : 0;
+        int e = u;  // 32 pairs' units fit
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(kAll, e, o);
+          const int y = __shfl_up_sync(kAll, e, o);
           if (lane >= o) e += y;
         }
         const unsigned hit = __ballot_sync(kAll, at + e > x);
@@ -246,21 +245,24 @@ __device__ __forceinline__ void pt_schedule(const PtArgs& a, int lane, Emit emit
           continue;
         }
         const int hl = __ffs(hit) - 1;
-        const long long u1 = at + __shfl_sync(kAll, e, hl), u0 = u1 - __shfl_sync(kAll, u, hl);
+        const long long u1 = at + __shfl_sync(kAll, e, hl), end = min(u1, x1);
+        const long long s0 = u1 - __shfl_sync(kAll, u, hl) + kPtStart;  // its first column tile
         it.r0 = (n_p - 1 - (i0 + hl)) * kPtPair;
-        it.t0 = (int)(x - u0);
-        it.t1 = (int)(min(u1, x1) - u0);
-        const long long fc = pg_div(u0, per), lc = pg_div(u1 - 1, per);
+        it.t0 = (int)max(0ll, x - s0);
+        it.t1 = (int)(end - s0);
+        const long long fc = pg_div(s0, per), lc = pg_div(u1 - 1, per);
         it.parts = (int)(lc - fc) + 1;
         // the first item of a block has its slot 0, the last, if it goes on behind the block, slot 1
-        it.slot = blockIdx.x * 2 + (fc == blockIdx.x && u0 != fc * per);
+        it.slot = blockIdx.x * 2 + (fc == blockIdx.x && s0 != fc * per);
+        x = end;
+        if (end <= s0) break;  // the next block has its column tiles
         if (it.parts > 1 && fc == blockIdx.x && lane == 0)
           a.cuts[blockIdx.x] = PgCut{it.parts, it.slot, it.h, it.q0, it.n, it.r0, {0, 0}};
-        x = min(u1, x1);
         break;
       }
+      if (it.t1 <= 0) continue;
       // a pair that sees no column has one unit and no tiles
-      it.t1 = min(it.t1, pt_tiles(it.n, it.L, G, it.r0 + kPtPair));
+      it.t1 = min(it.t1, pt_tiles(it.n, it.L, g, it.r0 + kPtPair));
       if (!emit(it)) return;
     }
     base += chunk_total;
@@ -268,10 +270,10 @@ __device__ __forceinline__ void pt_schedule(const PtArgs& a, int lane, Emit emit
 }
 
 // Column tiles of the item that tile x (0 = A, 1 = B) reads, from t0 on.
-__device__ __forceinline__ int pt_mine(const PtItem& it, int G, int x) {
+__device__ __forceinline__ int pt_mine(const PtItem& it, const PgArgs& g, int x) {
   const int first = it.r0 + x * kPtRows;
-  if (first >= it.n * G) return 0;
-  return max(0, min(it.t1, pt_tiles(it.n, it.L, G, first + kPtRows)) - it.t0);
+  if (first >= it.n * g.G) return 0;
+  return max(0, min(it.t1, pt_tiles(it.n, it.L, g, first + kPtRows)) - it.t0);
 }
 
 // Registers move from the warpgroups of the other roles to the rows', which
@@ -394,12 +396,13 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   } else if (warp == kPtWarpTma) {
     // ------------------------------------------------------------ K / V loads
     pt_regs_dec<kPtRegsRest>();
+    if (lane < 2) asm volatile("prefetch.tensormap [%0];\n" ::"l"(lane ? &tm_v : &tm_k) : "memory");
     const int box = 1 << a.box_shift, boxes = kPtCols >> a.box_shift;
     uint32_t seq = 0, tails = 0;
     bool ok = true;
     PtItem it;
     for (uint32_t k = 0; ok && next_item(k, it); ++k) {
-      const int nt = max(pt_mine(it, g.G, 0), pt_mine(it, g.G, 1));
+      const int nt = max(pt_mine(it, g, 0), pt_mine(it, g, 1));
       // lane l's page and first token in it, of box l of column tile t
       auto page_of = [&](int t) -> int {
         if (!g.table) return 0;
@@ -506,7 +509,7 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const PtItem it = items[k & 1];
         mbar_arrive(&item_empty[k & 1]);
         if (!it.valid) break;
-        const int mine[2] = {pt_mine(it, g.G, 0), pt_mine(it, g.G, 1)};
+        const int mine[2] = {pt_mine(it, g, 0), pt_mine(it, g, 1)};
         const int my = mine[x], nt = max(mine[0], mine[1]);
         if (!wait(&q_full[x], k & 1)) break;
         const uint32_t base = seq;
@@ -564,20 +567,15 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     // ------------------------------------------------------------ queries
     pt_regs_dec<kPtRegsRest>();
     constexpr int kPieces = DH / 8;
-    bool ok = true;
     PtItem it;
-    for (uint32_t k = 0; ok && next_item(k, it); ++k) {
+    for (uint32_t k = 0; next_item(k, it); ++k) {
       const int rows = it.n * g.G;
-      for (int x = 0; x < 2 && ok; ++x) {
-        if (k > 0 && !wait_warp(&q_empty[x], (k - 1) & 1)) {
-          ok = false;
-          break;
-        }
-        // a warp brings 32 rows, 16 bytes a lane; lane l knows where row l lies
+      // a warp brings 32 rows of a tile, 16 bytes a lane; lane l knows where row l lies
+      auto bring = [&](int x) {
         const int mine = it.r0 + x * kPtRows + (warp - kPtWarpQ) * 32 + lane;
         const uint16_t* at = nullptr;
         if (mine < rows) {
-          const int tok = mine / g.G;
+          const int tok = g.by_g(mine);
           at = g.q.p + (it.q0 + tok) * g.q.st + (long long)(it.h * g.G + mine - tok * g.G) * g.q.sh;
         }
         const unsigned long long mine_at = reinterpret_cast<unsigned long long>(at);
@@ -589,10 +587,28 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           cp_async16(smem + x * C::kQBytes + (c >> 3) * C::kQChunk + row * 128 + (((c & 7) ^ (row & 7)) << 4),
                      src ? reinterpret_cast<const uint16_t*>(src) + c * 8 : g.q.p, src ? 16 : 0);
         }
-        cp_async_wait_all();
+        cp_async_commit();
+      };
+      auto hand_on = [&](int x) {
         fence_proxy_async_smem();
         mbar_arrive(&q_full[x]);
+      };
+      if (k > 0 && !wait_warp(&q_empty[0], (k - 1) & 1)) break;
+      bring(0);
+      // tile B's with them, if its place is free already
+      const bool both = k == 0 || __all_sync(0xffffffffu, mbar_try_wait(&q_empty[1], (k - 1) & 1));
+      if (both) {
+        bring(1);
+        cp_async_wait<1>();
+        hand_on(0);
+      } else {
+        cp_async_wait<0>();
+        hand_on(0);
+        if (!wait_warp(&q_empty[1], (k - 1) & 1)) break;
+        bring(1);
       }
+      cp_async_wait<0>();
+      hand_on(1);
     }
   } else {
     // ------------------------------------------------------------ rows
@@ -625,12 +641,12 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         release();
         break;
       }
-      const int my = pt_mine(it, g.G, x);
+      const int my = pt_mine(it, g, x);
       // columns of the item's that the row sees; a row behind the last one computes on zero queries and is not written
       int seen = 0x7fffffff;
       {
         const int r = it.r0 + x * kPtRows + row;
-        if (r < it.n * g.G) seen = it.L - it.n + r / g.G + 1 - it.t0 * kPtCols;
+        if (r < it.n * g.G) seen = it.L - it.n + g.by_g(r) + 1 - it.t0 * kPtCols;
       }
       float m_ref = -INFINITY, z = 0.f;
       for (int t = 0; t < my && ok; ++t, ++u) {
@@ -649,6 +665,8 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           }
           // The exponentials are taken on the reference as it is, beside the maximum that says
           // whether it will do: one score in thousands of tiles says no, and they are taken again.
+          // (An item's first ones always are: making them wait for the maximum made every other
+          // half 5% slower, since the two no longer run beside each other.)
           uint32_t pk[32];
           uint64_t za[2];
           auto exps = [&]() {
@@ -706,7 +724,7 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       full += my > 0;
       const int r = it.r0 + x * kPtRows + row;
       const bool live = r < it.n * g.G;
-      const int tok = r / g.G, hq = it.h * g.G + r - tok * g.G;
+      const int tok = g.by_g(r), hq = it.h * g.G + r - tok * g.G;
       // write-back; a numerator is read once for all rows of the warp, whether live or not
       const float inv = z == 0.f ? 0.f : 1.f / z;
       uint16_t* od = g.o.p + (live ? (it.q0 + tok) * g.o.st + (long long)hq * g.o.sh : 0);
@@ -729,16 +747,23 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           g.lse[(size_t)hq * g.max_tokens + it.q0 + tok] = zz == 0.f ? -INFINITY : (m + log2f(zz)) * kPgLn2;
       };
       const size_t prow = (size_t)it.slot * kPtPair + x * kPtRows + row;
-#pragma unroll 1
-      for (int cc = 0; cc < DH; cc += 32) {
-        uint32_t w[32];
+      uint32_t w[2][32];
+      if (my > 0) tmem_ld32(nbase, w[0]);
+#pragma unroll
+      for (int i = 0; i < DH / 32; ++i) {
+        const int cc = 32 * i;
         float v[32];
         if (my > 0) {
-          tmem_ld32(nbase + cc, w);
           tmem_wait_ld();
+          if (cc + 32 < DH) tmem_ld32(nbase + cc + 32, w[(i + 1) & 1]);
+        }
+        if (cc + 32 == DH) {  // the numerator is free for the next item's
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&n_free[x]);
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = my > 0 ? __uint_as_float(w[e]) : 0.f;
+        for (int e = 0; e < 32; ++e) v[e] = my > 0 ? __uint_as_float(w[i & 1][e]) : 0.f;
         if (it.parts == 1) {
           put(cc, v);
         } else if (live && my > 0) {
@@ -748,9 +773,6 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             __stcg(d + e * kPtPair, make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&n_free[x]);
       if (it.parts == 1) {
         put_lse(m_ref, z);
         release();
@@ -767,7 +789,6 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (threadIdx.x == 0) pg_wait_for_launch_before();
 }
 
 int at_sm_count();
@@ -799,10 +820,9 @@ static int pt_tmap(CUtensorMap* map, const PgPages& t, int bf16, uint64_t dh, ui
   return r == CUDA_SUCCESS ? FLASHLOOP_OK : FLASHLOOP_ERR_CUDA;
 }
 
-int launch_pg_tile(const PgArgs& g, int dh, int bf16, int few, const PgScratch& ws, bool early, cudaStream_t stream) {
+int launch_pg_tile(const PgArgs& g, int dh, int bf16, const PgScratch& ws, cudaStream_t stream) {
   PtArgs a{};
   a.g = g;
-  a.few = few;
   a.box_shift = g.table && g.shift < 7 ? g.shift : 7;
   a.cuts = ws.tile_cuts;
   a.part_mz = ws.tile_mz;
@@ -822,7 +842,6 @@ int launch_pg_tile(const PgArgs& g, int dh, int bf16, int few, const PgScratch& 
   }
   auto go = [&](auto kernel, int smem) -> int {
     FL_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    if (early) return pg_launch_early(kernel, dim3(grid), kPtThreads, smem, stream, tk, tv, a);
     kernel<<<grid, kPtThreads, smem, stream>>>(tk, tv, a);
     return launch_status();
   };
