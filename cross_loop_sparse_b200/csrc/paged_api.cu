@@ -7,7 +7,7 @@
 namespace fl {
 
 int check_device_arch();
-int launch_paged_plan(const flashloop_paged_params*, int, const int32_t*, const int32_t*, const int32_t*,
+int launch_paged_plan(const flashloop_paged_params*, int, const int32_t*, const int32_t*, const int32_t*, int,
                       const int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*,
                       cudaStream_t);
 int launch_paged_kv_write(const flashloop_paged_params*, int, const flashloop_rows*, const flashloop_rows*, int,
@@ -43,7 +43,7 @@ static int pg_check_heads(const flashloop_paged_params* p, bool queries) {
   if (!queries) return FLASHLOOP_OK;
   if (p->n_heads < 1 || p->n_heads % p->n_kv_heads != 0) return FLASHLOOP_ERR_INVALID_ARG;
   if ((long long)p->max_tokens * p->n_heads > 0x7fffffffll) return FLASHLOOP_ERR_UNSUPPORTED;  // packed rows are 32-bit
-  if (!isfinite(p->scale) || !(p->scale > 0.f)) return FLASHLOOP_ERR_INVALID_ARG;
+  if (!isfinite(p->scale * kPgLog2e) || !(p->scale > 0.f)) return FLASHLOOP_ERR_INVALID_ARG;
   return FLASHLOOP_OK;
 }
 
@@ -132,13 +132,14 @@ using namespace fl;
 extern "C" {
 
 int flashloop_paged_plan(const flashloop_paged_params* p, const int32_t* kv_lens, const int32_t* new_lens,
-                         const int32_t* free_pages, const int32_t* n_free, int32_t* block_table, int32_t* cu,
-                         int32_t* kv_lens_out, int32_t* slot_map, int32_t* positions, int32_t* n_free_out,
-                         int32_t* err_word, void* stream) {
+                         const int32_t* free_pages, int32_t free_capacity, const int32_t* n_free,
+                         int32_t* block_table, int32_t* cu, int32_t* kv_lens_out, int32_t* slot_map,
+                         int32_t* positions, int32_t* n_free_out, int32_t* err_word, void* stream) {
   int rc = pg_check_sizes(p);
   if (rc == FLASHLOOP_OK) rc = pg_check_pages(p);
   if (rc != FLASHLOOP_OK) return rc;
-  if (!free_pages || !n_free || !cu || !n_free_out) return FLASHLOOP_ERR_INVALID_ARG;
+  if (!n_free || !cu || !n_free_out || free_capacity < 0 || (free_capacity > 0 && !free_pages))
+    return FLASHLOOP_ERR_INVALID_ARG;
   if (p->batch > 0 && (!kv_lens || !new_lens || !block_table || !kv_lens_out)) return FLASHLOOP_ERR_INVALID_ARG;
   if (p->max_tokens > 0 && (!slot_map || !positions)) return FLASHLOOP_ERR_INVALID_ARG;
   // every block reads the lengths while block 0 writes the new ones
@@ -149,8 +150,8 @@ int flashloop_paged_plan(const flashloop_paged_params* p, const int32_t* kv_lens
     return FLASHLOOP_ERR_INVALID_ARG;
   rc = check_device_arch();
   if (rc != FLASHLOOP_OK) return rc;
-  return launch_paged_plan(p, pg_shift(p->page_size), kv_lens, new_lens, free_pages, n_free, block_table, cu,
-                           kv_lens_out, slot_map, positions, n_free_out, err_word,
+  return launch_paged_plan(p, pg_shift(p->page_size), kv_lens, new_lens, free_pages, free_capacity, n_free, block_table,
+                           cu, kv_lens_out, slot_map, positions, n_free_out, err_word,
                            reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -16,7 +16,7 @@ constexpr int kPlanThreads = 512;
 constexpr int kPlanTokens = 1024;  // tokens a block takes at least
 
 struct PlanArgs {
-  int B, T, shift, n_pages, max_blocks;
+  int B, T, shift, n_pages, max_blocks, max_free;
   const int32_t* kv;
   const int32_t* add;
   const int32_t* stack;
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs g) {
   __syncthreads();
   const int n_free = *g.n_free;
   int code = 0;
-  if ((s_bad & FLASHLOOP_DEVERR_INDEX) || n_free < 0 || n_free > g.n_pages) code = FLASHLOOP_DEVERR_INDEX;
+  if ((s_bad & FLASHLOOP_DEVERR_INDEX) || n_free < 0 || n_free > g.max_free) code = FLASHLOOP_DEVERR_INDEX;
   else if (s_bad || s_new > (unsigned long long)g.T || s_opened > (unsigned long long)n_free)
     code = FLASHLOOP_DEVERR_CAPACITY;
   const int total = code ? 0 : (int)s_new;
@@ -147,10 +147,11 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs g) {
 }
 
 int launch_paged_plan(const flashloop_paged_params* p, int shift, const int32_t* kv_lens, const int32_t* new_lens,
-                      const int32_t* free_pages, const int32_t* n_free, int32_t* table, int32_t* cu,
+                      const int32_t* free_pages, int free_capacity, const int32_t* n_free, int32_t* table, int32_t* cu,
                       int32_t* kv_lens_out, int32_t* slot_map, int32_t* positions, int32_t* n_free_out, int32_t* err,
                       cudaStream_t stream) {
-  PlanArgs g{p->batch, p->max_tokens, shift, p->n_pages, p->max_blocks, kv_lens, new_lens, free_pages, n_free,
+  PlanArgs g{p->batch, p->max_tokens, shift, p->n_pages, p->max_blocks,
+             free_capacity < p->n_pages ? free_capacity : p->n_pages, kv_lens, new_lens, free_pages, n_free,
              table, cu, kv_lens_out, slot_map, positions, n_free_out, err};
   int grid = (p->max_tokens + kPlanTokens - 1) / kPlanTokens;
   if (grid > 148) grid = 148;

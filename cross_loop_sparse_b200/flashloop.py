@@ -164,7 +164,7 @@ _SIG = {
     "flashloop_check_error_word": (_I, [_V, POINTER(c_int32), _V]),
     "flashloop_selftest_bounded_wait": (_I, [_I, _V, _V]),
     "flashloop_status_string": (ctypes.c_char_p, [_I]),
-    "flashloop_paged_plan": (_I, [_PP, _V, _V, _V, _V, _V, _V, _V, _V, _V, _V, _V, _V]),
+    "flashloop_paged_plan": (_I, [_PP, _V, _V, _V, _I, _V, _V, _V, _V, _V, _V, _V, _V, _V]),
     "flashloop_paged_kv_write": (_I, [_PP, _RW, _RW, _I, _V, _PG, _PG, _V, _V]),
     "flashloop_prompt_attn": (_I, [_PP, _RW, _RW, _RW, _V, _RW, _V, _V, _V]),
     "flashloop_paged_attn_workspace_bytes": (c_size_t, [_PP]),
@@ -431,7 +431,7 @@ def flashloop_paged_plan(params, kv_lens, new_lens, free_pages, n_free, block_ta
     B, T = max(p.batch, 0), max(p.max_tokens, 0)
     return _launch(fn, dev, stream, ctypes.byref(p), _vec(fn, "kv_lens", kv_lens, B, i32, dev),
                    _vec(fn, "new_lens", new_lens, B, i32, dev),
-                   _vec(fn, "free_pages", free_pages, 0, i32, dev), _vec(fn, "n_free", n_free, 1, i32, dev),
+                   _vec(fn, "free_pages", free_pages, 0, i32, dev), free_pages.numel(), _vec(fn, "n_free", n_free, 1, i32, dev),
                    _vec(fn, "block_table", block_table, B * p.max_blocks, i32, dev),
                    _vec(fn, "cu", cu, B + 1, i32, dev), _vec(fn, "kv_lens_out", kv_lens_out, B, i32, dev),
                    _vec(fn, "slot_map", slot_map, T, i32, dev), _vec(fn, "positions", positions, T, i32, dev),

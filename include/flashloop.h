@@ -539,7 +539,7 @@ typedef struct flashloop_pages {
 
 /* Block tables and slot maps from request lengths.  Request b holds kv_lens[b]
  * tokens and appends new_lens[b] >= 0.  free_pages[0..*n_free) is a stack of
- * free pages; pages are taken from its top, in request order, for the blocks
+ * free pages in a buffer of free_capacity entries; pages are taken from its top, in request order, for the blocks
  * that the new tokens open:
  *   cu[b] = sum of new_lens[0..b) (cu[batch] the total),
  *   kv_lens_out[b] = kv_lens[b] + new_lens[b],
@@ -550,16 +550,16 @@ typedef struct flashloop_pages {
  *   *n_free_out = *n_free - pages taken.
  * All or nothing: too few free pages, more than max_tokens tokens or more than
  * max_blocks blocks set FLASHLOOP_DEVERR_CAPACITY, a negative length or a
- * count of free pages outside [0, n_pages] FLASHLOOP_DEVERR_INDEX, and then the
+ * count of free pages outside [0, min(n_pages, free_capacity)] FLASHLOOP_DEVERR_INDEX, and then the
  * call appends nothing: cu is 0, kv_lens_out = kv_lens, *n_free_out = *n_free
  * and every slot -1.  A page id outside [0, n_pages) on the stack or in the
  * table sets FLASHLOOP_DEVERR_INDEX and gives its tokens slot -1.  The pages
  * of a finished request go back by writing them at free_pages[*n_free...).
  * kv_lens_out and n_free_out do not overlap the inputs. */
 int flashloop_paged_plan(const flashloop_paged_params* p, const int32_t* kv_lens, const int32_t* new_lens,
-                         const int32_t* free_pages, const int32_t* n_free, int32_t* block_table, int32_t* cu,
-                         int32_t* kv_lens_out, int32_t* slot_map, int32_t* positions, int32_t* n_free_out,
-                         int32_t* err_word, void* stream);
+                         const int32_t* free_pages, int32_t free_capacity, const int32_t* n_free,
+                         int32_t* block_table, int32_t* cu, int32_t* kv_lens_out, int32_t* slot_map,
+                         int32_t* positions, int32_t* n_free_out, int32_t* err_word, void* stream);
 
 /* Write the keys and values of max_tokens rows into the pages of their slots,
  * rounded to params.dtype (nearest, ties to even).  src_dtype is params.dtype

@@ -85,7 +85,7 @@ def test_plan_matches_the_definition(held, new, page, pad):
 
 @pytest.mark.parametrize("held,new,cut,code", [
     ([3, 20], [30, 9], "pages", 1), ([3, 20], [30, 9], "tokens", 1), ([3, 20], [30, 9], "blocks", 1), ([3, 20], [30, -1], "", 2), ([-4, 20], [30, 1], "", 2),
-    ([2147483647, 0], [2147483647, 1], "", 1),
+    ([2147483647, 0], [2147483647, 1], "", 1), ([3, 20], [30, 9], "count", 2),
 ])
 def test_plan_appends_all_or_nothing(held, new, cut, code):
     page = 16
@@ -94,7 +94,10 @@ def test_plan_appends_all_or_nothing(held, new, cut, code):
     T -= cut == "tokens"
     width = 2 if cut == "blocks" else width
     table = [r[:width] for r in table]
-    c = Plan(held, new, table, stack, page, n_pages, width, T).run()
+    c = Plan(held, new, table, stack, page, n_pages, width, T)
+    if cut == "count":  # more free pages than the buffer holds
+        c.stack = c.stack[:len(stack) - 1].contiguous()
+    c.run()
     assert c.err.item() == code
     assert c.cu.tolist() == [0, 0, 0] and c.kv_out.tolist() == held and c.n_out.tolist() == [len(stack)]
     assert c.table.tolist() == table

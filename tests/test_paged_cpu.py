@@ -57,7 +57,7 @@ def test_bad_parameters_are_refused_before_any_device_query():
     R, P, B = ctypes.byref(rows), ctypes.byref(pages), ctypes.byref
 
     def plan(p):
-        return F._lib.flashloop_paged_plan(B(p), a, a, a, a, a, a, ctypes.c_void_p(8192), a, a, ctypes.c_void_p(12288), a, None)
+        return F._lib.flashloop_paged_plan(B(p), a, a, a, 100, a, a, a, ctypes.c_void_p(8192), a, a, ctypes.c_void_p(12288), a, None)
 
     def write(p):
         return F._lib.flashloop_paged_kv_write(B(p), R, R, p.dtype, a, P, P, a, None)
@@ -112,12 +112,12 @@ def test_bad_arguments_are_refused_before_any_device_query():
     # float32 rows: strides of 16 bytes are multiples of four elements
     assert write(k=F.RowsC(4096, 1026, 128), src=2) == -1
     # plan: a missing buffer, and new lengths that lie over the old
-    args = [a, a, a, a, a, a, ctypes.c_void_p(8192), a, a, ctypes.c_void_p(12288)]
-    for i in range(10):
+    args = [a, a, a, 100, a, a, a, ctypes.c_void_p(8192), a, a, ctypes.c_void_p(12288)]
+    for i in range(11):
         some = list(args)
-        some[i] = None
+        some[i] = -1 if i == 3 else None
         assert F._lib.flashloop_paged_plan(B(p), *some, a, None) == -1, i
-    for i, over in ((6, 4096), (6, 4096 + 12), (9, 4096)):
+    for i, over in ((7, 4096), (7, 4096 + 12), (10, 4096)):
         some = list(args)
         some[i] = ctypes.c_void_p(over)
         assert F._lib.flashloop_paged_plan(B(p), *some, a, None) == -1, (i, over)
