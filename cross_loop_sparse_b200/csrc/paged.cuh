@@ -129,12 +129,7 @@ inline int pg_launch_early(Kernel kernel, dim3 grid, int threads, size_t smem, c
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? FLASHLOOP_OK : FLASHLOOP_ERR_CUDA;
 }
 
-// A call whose requests have at most this many packed rows (max_new x group) is
-// the few-row kernel's, any other the tile kernel's, whole: short requests among
-// long ones cost a tile kernel's block no more than HBM takes to bring their keys
-// and values (3000 cycles a 128-column tile against 2700), while a second kernel
-// for them comes on top: 255 us against 248 us for 32 decoding requests beside two
-// chunks of 1500 rows, and a launch that does nothing where none decodes.
+// Rows of a slot of the few-row kernel, its largest row tile.
 constexpr int kPgFewRows = 32;
 
 // Tables of at most this many columns are not cut: whole requests are a few

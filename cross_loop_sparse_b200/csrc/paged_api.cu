@@ -6,6 +6,10 @@
 
 namespace fl {
 
+// Microseconds of the kernels' parts, for the choice between them.
+constexpr double kPgFewStart = 4.0, kPgFewCut = 9.0, kPgFewStage = 0.8;
+constexpr double kPgTileStart = 8.0, kPgTileCut = 16.0, kPgTileUnit = 1.9;
+
 int check_device_arch();
 int launch_paged_plan(const flashloop_paged_params*, int, const int32_t*, const int32_t*, const int32_t*, int,
                       const int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*,
@@ -77,9 +81,27 @@ static bool pg_tma_ok(const PgArgs& g, int pages) {
   return true;
 }
 
-static bool pg_tiles(const flashloop_paged_params* p) {
+// Which kernel takes a call whose requests see at most `cols` columns, by its
+// bounds alone: an estimate of both times in microseconds.  A block of the few-row
+// kernel takes a stage of 64 columns for 32 packed rows, one of the tile kernel
+// 128 columns for 256 rows; both start, and join what is cut, at a price.
+static bool pg_tiles(const flashloop_paged_params* p, long long cols, bool cut) {
   const long long most = p->max_new < p->max_tokens ? p->max_new : p->max_tokens;
-  return most * (p->n_heads / p->n_kv_heads) > kPgFewRows;
+  const long long group = p->n_heads / p->n_kv_heads;
+  if (most * group <= kPgFewRows) return false;
+  const double rows = (double)p->max_tokens * p->n_heads;
+  const double starts = (double)(p->batch < p->max_tokens ? p->batch : p->max_tokens) * p->n_kv_heads;
+  const double few = rows / kPgFewRows + starts, tiles = rows / kPgTileRows + starts;  // row tiles at most
+  const double stages = (double)((cols + 63) / 64), units = (double)((cols + 127) / 128);
+  auto waves = [](double n, double blocks) { return n <= blocks ? 1.0 : n / blocks; };
+  const double few_us = cut ? kPgFewCut + kPgFewStage * (few * stages / (2 * kPgSms) > 4 ? few * stages / (2 * kPgSms) : 4)
+                            : kPgFewStart + kPgFewStage * stages * waves(few, 2 * kPgSms);
+  const double tile_us = cut ? kPgTileCut + kPgTileUnit * (tiles * units / kPgSms > 4 ? tiles * units / kPgSms : 4)
+                             : kPgTileStart + kPgTileUnit * units * waves(tiles, kPgSms);
+  return tile_us < few_us;
+}
+static bool pg_tiles(const flashloop_paged_params* p) {
+  return pg_tiles(p, (long long)p->max_blocks * p->page_size, true);
 }
 
 // Offsets depend on the shape alone.
@@ -188,7 +210,7 @@ int flashloop_prompt_attn(const flashloop_paged_params* p, const flashloop_rows*
   g.v = {static_cast<const uint16_t*>(v->data), 0, v->stride_token, v->stride_head};
   const int bf16 = p->dtype == FLASHLOOP_DTYPE_BF16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!pg_tma_ok(g, 1)) return launch_pg_rows(g, p->head_dim, bf16, PgScratch{}, s);
+  if (!pg_tiles(p, g.max_new, false) || !pg_tma_ok(g, 1)) return launch_pg_rows(g, p->head_dim, bf16, PgScratch{}, s);
   return launch_pg_tile(g, p->head_dim, bf16, PgScratch{}, s);
 }
 

@@ -93,7 +93,7 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
       }
     }
 
-  const int stages = (ncols - s.c0 + kPrCols - 1) / kPrCols;
+  const int stages = ncols > s.c0 ? (ncols - s.c0 + kPrCols - 1) / kPrCols : 0;
   // the page of this warp's slice of stages [32 i, 32 i + 32): lane l holds stage 32 i + l
   auto pages_of = [&](int st) -> int {
     const int col = s.c0 + st * kPrCols + warp * 16;
@@ -288,9 +288,11 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
   }
 }
 
-// Units of one key head of request s; a request whose rows see nothing still has them written.
-__device__ __forceinline__ int pr_units(const PgSeq& s) {
-  return s.n > 0 ? kPrStart + max(1, (s.L + kPrCols - 1) / kPrCols) : 0;
+// Units of a row tile of request s (a request whose rows see nothing still has them written), and
+// the request's row tiles of one key head.
+__device__ __forceinline__ int pr_units(const PgSeq& s) { return kPrStart + max(1, (s.L + kPrCols - 1) / kPrCols); }
+__device__ __forceinline__ int pr_tiles(const PgArgs& g, const PgSeq& s) {
+  return (s.n * g.G + kPgFewRows - 1) / kPgFewRows;
 }
 
 template <int DH, int BF, int MT>
@@ -312,11 +314,12 @@ __global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PrArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // a thread's request of the chunk at b0, and sums over the chunk: inclusive and whole
   PgSeq q;
-  long long incl, whole;
+  long long mine, incl, whole;
   auto chunk = [&](int b0) {
     q = {0, 0, 0};
     if (b0 + tid < g.B) q = pg_seq(g, b0 + tid);
-    incl = pr_units(q);
+    incl = (long long)pr_units(q) * pr_tiles(g, q);
+    mine = incl;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -347,7 +350,7 @@ __global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PrArgs a) {
   long long base = 0;
   for (int b0 = 0; b0 < g.B; b0 += kPrThreads) {
     if (g.B > kPrThreads) chunk(b0);
-    const long long first = base + (incl - pr_units(q)) * g.Hk;
+    const long long first = base + (incl - mine) * g.Hk;
     if (x >= first && x < base + incl * g.Hk) {
       s_b = b0 + tid;
       s_at = first;
@@ -360,35 +363,39 @@ __global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PrArgs a) {
   long long at = s_at;  // the request's first unit
   while (x < x1) {
     q = pg_seq(g, b);
-    const int u = pr_units(q);
-    while (x < x1 && x < at + (long long)u * g.Hk) {
+    const int u = pr_units(q), tiles = pr_tiles(g, q);
+    const long long next = at + (long long)u * tiles * g.Hk;
+    while (x < x1 && x < next) {
       PrItem it{};
       it.b = b;
-      it.h = (int)pg_div(x - at, u);
+      const int idx = (int)pg_div(x - at, u);  // key head by key head, the row tiles of one next to each other
+      it.h = idx / tiles;
+      it.r0 = (idx - it.h * tiles) * kPgFewRows;
       it.q0 = q.q0;
       it.n = q.n;
       it.L = q.L;
-      const long long u1 = at + (long long)(it.h + 1) * u, end = min(u1, x1);
+      const long long u1 = at + (long long)(idx + 1) * u, end = min(u1, x1);
       const long long s0 = u1 - u + kPrStart;  // its first stage
       if (end <= s0) {  // the next block has its stages
         x = end;
         break;
       }
       it.c0 = (int)max(0ll, x - s0) * kPrCols;
-      it.c1 = min(q.L, (int)(end - s0) * kPrCols);
+      const int last = min(q.n * g.G, it.r0 + kPgFewRows) - 1;  // its last row, which sees the most
+      it.c1 = max(0, min(q.L - q.n + g.by_g(last) + 1, (int)(end - s0) * kPrCols));
       const long long fc = pg_div(s0, per), lc = pg_div(u1 - 1, per);
       it.parts = (int)(lc - fc) + 1;
       // the first item of a block has its slot 0, the last, if it goes on behind the block, slot 1
       it.slot = blockIdx.x * 2 + (fc == blockIdx.x && s0 != fc * per);
       if (it.parts > 1 && fc == blockIdx.x && tid == 0)
-        a.cuts[blockIdx.x] = PgCut{it.parts, it.slot, it.h, it.q0, it.n, 0, {0, 0}};
+        a.cuts[blockIdx.x] = PgCut{it.parts, it.slot, it.h, it.q0, it.n, it.r0, {0, 0}};
       // a request of one row tile does half of the products
       if (MT == 2 && q.n * g.G <= 16) pr_item<DH, BF, 1>(a, it, smem);
       else pr_item<DH, BF, MT>(a, it, smem);
       __syncthreads();  // shared memory goes to the next item
       x = end;
     }
-    at += (long long)u * g.Hk;
+    at = next;
     ++b;
   }
 }
