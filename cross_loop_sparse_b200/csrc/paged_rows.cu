@@ -108,6 +108,17 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
   };
   int pages = pages_of(lane), pages_next = pages_of(32 + lane);
   const long long row0 = g.table ? 0 : s.q0;
+  // A lane brings 16 bytes of every kStep-th row of K and of V, beginning with row `up`; row r's
+  // 16-byte piece c lies at place c ^ (r & 7), so that ldmatrix's eight rows fall on all banks.
+  // The addresses advance by a constant a copy (computed anew for each of them, with a check a
+  // row, issuing took 530 to 1380 cycles a stage, as much as everything else); the last columns
+  // and bad pages take the checks.
+  constexpr int kStep = 32 / kPieces;
+  const int up = lane / kPieces, piece = lane % kPieces;
+  const uint32_t to = smem_u32(ring) + up * (DH * 2);
+  const uint16_t* k_lane = g.k.p + h * g.k.sh + (row0 + up) * g.k.st + piece * 8;
+  const uint16_t* v_lane = g.v.p + h * g.v.sh + (row0 + up) * g.v.st + piece * 8;
+  const long long k_step = kStep * g.k.st, v_step = kStep * g.v.st;
   auto load = [&](int st) {
     if (st < stages) {
       if ((st & 31) == 0 && st > 0) {
@@ -117,16 +128,28 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
       const int page = __shfl_sync(0xffffffffu, pages, st & 31);
       const int c0 = s.c0 + st * kPrCols + warp * 16;
       const int in0 = g.table ? (c0 & ((1 << shift) - 1)) : c0;
-      uint8_t* dst = ring + (st % C::kStages) * 2 * C::kTile;
-      const uint16_t* kb = g.k.p + (page > 0 ? page : 0) * g.k.sp + (row0 + in0) * g.k.st + h * g.k.sh;
-      const uint16_t* vb = g.v.p + (page > 0 ? page : 0) * g.v.sp + (row0 + in0) * g.v.st + h * g.v.sh;
+      const uint32_t dst = to + (st % C::kStages) * 2 * C::kTile;
+      const uint16_t* ks = k_lane + (page > 0 ? page : 0) * g.k.sp + in0 * g.k.st;
+      const uint16_t* vs = v_lane + (page > 0 ? page : 0) * g.v.sp + in0 * g.v.st;
+      if (page >= 0 && c0 + 16 <= ncols) {
 #pragma unroll
-      for (int it = 0; it < 16 * kPieces / 32; ++it) {
-        const int i = it * 32 + lane, row = i / kPieces, c = i % kPieces;
-        const int bytes = (page >= 0 && c0 + row < ncols) ? 16 : 0;  // the rest reads as zero
-        const uint32_t at = row * DH * 2 + ((c ^ (row & 7)) << 4);
-        cp_async16(dst + at, bytes ? kb + row * g.k.st + c * 8 : g.k.p, bytes);
-        cp_async16(dst + C::kTile + at, bytes ? vb + row * g.v.st + c * 8 : g.v.p, bytes);
+        for (int it = 0; it < 16 / kStep; ++it) {
+          const uint32_t at = dst + it * kStep * DH * 2 + ((piece ^ ((it * kStep + up) & 7)) << 4);
+          cp_async16_to(at, ks);
+          cp_async16_to(at + C::kTile, vs);
+          ks += k_step;
+          vs += v_step;
+        }
+      } else {
+#pragma unroll 1
+        for (int it = 0; it < 16 / kStep; ++it) {
+          const uint32_t at = dst + it * kStep * DH * 2 + ((piece ^ ((it * kStep + up) & 7)) << 4);
+          const int bytes = (page >= 0 && c0 + it * kStep + up < ncols) ? 16 : 0;  // the rest reads as zero
+          cp_async16_to(at, bytes ? ks : g.k.p, bytes);
+          cp_async16_to(at + C::kTile, bytes ? vs : g.v.p, bytes);
+          ks += k_step;
+          vs += v_step;
+        }
       }
     }
     cp_async_commit();
