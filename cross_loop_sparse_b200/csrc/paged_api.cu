@@ -6,10 +6,6 @@
 
 namespace fl {
 
-// Microseconds of the kernels' parts, for the choice between them.
-constexpr double kPgFewStart = 4.0, kPgFewCut = 9.0, kPgFewStage = 0.8;
-constexpr double kPgTileStart = 8.0, kPgTileCut = 16.0, kPgTileUnit = 1.9;
-
 int check_device_arch();
 int launch_paged_plan(const flashloop_paged_params*, int, const int32_t*, const int32_t*, const int32_t*, int,
                       const int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*,
@@ -81,24 +77,37 @@ static bool pg_tma_ok(const PgArgs& g, int pages) {
   return true;
 }
 
-// Which kernel takes a call whose requests see at most `cols` columns, by its
-// bounds alone: an estimate of both times in microseconds.  A block of the few-row
-// kernel takes a stage of 64 columns for 32 packed rows, one of the tile kernel
-// 128 columns for 256 rows; both start, and join what is cut, at a price.
-static bool pg_tiles(const flashloop_paged_params* p, long long cols, bool cut) {
+// Which kernel takes a call whose requests see at most `cols` columns, by the
+// call's bounds alone: estimates of both times in microseconds, fitted to both
+// kernels' times over 35 shapes.  A block of the few-row kernel takes a stage of
+// 64 columns for 32 packed rows (two blocks an SM), one of the tile kernel 128
+// columns for 256 rows; to start and, where the column line is cut, to join has a
+// price for each.  Some of those times (few-row / tile kernel):
+//   prompts   24 rows, 2 heads a key head, of 16 tokens: 7.2 / 8.5
+//             1 x 512 tokens, 4 heads: 13.8 / 15.0     1 x 1024, 8 heads: 27.0 / 22.7
+//             4 x 512, 16 heads: 48.7 / 17.4           64 x 64, 16 heads: 56 / 18.7
+//   chunks    12 rows x 8 heads a key head over 2219: 18.1 / 20.7
+//             128 rows x 4 over 4096, 8 key heads: 49.4 / 31.9
+//             63 single rows and one of 64 over 8000 each, 32 heads: 389 / 447
+static bool pg_tiles(const flashloop_paged_params* p, long long cols, bool paged) {
   const long long most = p->max_new < p->max_tokens ? p->max_new : p->max_tokens;
-  const long long group = p->n_heads / p->n_kv_heads;
-  if (most * group <= kPgFewRows) return false;
+  if (most * (p->n_heads / p->n_kv_heads) <= kPgFewRows) return false;
+  auto over = [](double a, double b) { return a > b ? a : b; };
   const double rows = (double)p->max_tokens * p->n_heads;
-  const double starts = (double)(p->batch < p->max_tokens ? p->batch : p->max_tokens) * p->n_kv_heads;
-  const double few = rows / kPgFewRows + starts, tiles = rows / kPgTileRows + starts;  // row tiles at most
+  const double requests = p->batch < p->max_tokens ? p->batch : p->max_tokens;
+  const double starts = requests * p->n_kv_heads / 2;  // row tiles that a request does not fill
+  const double few = rows / kPgFewRows + starts, tiles = rows / kPgTileRows + starts;
   const double stages = (double)((cols + 63) / 64), units = (double)((cols + 127) / 128);
-  auto waves = [](double n, double blocks) { return n <= blocks ? 1.0 : n / blocks; };
-  const double few_us = cut ? kPgFewCut + kPgFewStage * (few * stages / (2 * kPgSms) > 4 ? few * stages / (2 * kPgSms) : 4)
-                            : kPgFewStart + kPgFewStage * stages * waves(few, 2 * kPgSms);
-  const double tile_us = cut ? kPgTileCut + kPgTileUnit * (tiles * units / kPgSms > 4 ? tiles * units / kPgSms : 4)
-                             : kPgTileStart + kPgTileUnit * units * waves(tiles, kPgSms);
-  return tile_us < few_us;
+  const double stage = p->head_dim == 128 ? 1.4 : 0.6, unit = p->head_dim == 128 ? 1.9 : 1.6;
+  const double blocks = 2 * kPgSms, sms = kPgSms;
+  if (!paged) {  // whole items; a prompt's row tiles see half of its columns on average
+    const double few_us = over(3.0 + stage * stages, few / blocks * (7.5 + stage / 2 * stages));
+    return over(7.0 + unit * units, tiles / sms * (7.0 + unit / 2 * units)) < few_us;
+  }
+  const double hbm = requests * (double)cols * p->n_kv_heads * p->head_dim * 4 / 6.5e6;
+  const double few_us = cols <= kPgShort ? over(3.0 + stage * stages, few / blocks * (7.5 + stage * stages))
+                                         : 9.0 + over(1.2 * stage * over(4.0, few * (stages + 6) / blocks), 1.15 * hbm);
+  return 18.0 + over(1.05 * unit * over(4.0, tiles * (units + 2) / sms), 1.35 * hbm) < few_us;
 }
 static bool pg_tiles(const flashloop_paged_params* p) {
   return pg_tiles(p, (long long)p->max_blocks * p->page_size, true);

@@ -193,23 +193,23 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
       }
     }
     uint32_t pa[MT][4];
+    if (c0 + 16 > free_cols) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c0 + n * 8 + (lane & 3) * 2 + (e & 1) > lim[mt][e >> 1]) sc[mt][n][e] = -INFINITY;
+    }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int col = c0 + n * 8 + (lane & 3) * 2 + (e & 1);
-          float x = sc[mt][n][e] * g.scale_log2;
-          if (c0 + 16 > free_cols && col > lim[mt][e >> 1]) x = -INFINITY;
-          sc[mt][n][e] = x;
-          mx[e >> 1] = fmaxf(mx[e >> 1], x);
-        }
+      float mx[2];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
+        mx[hf] = fmaxf(fmaxf(sc[mt][0][2 * hf], sc[mt][0][2 * hf + 1]), fmaxf(sc[mt][1][2 * hf], sc[mt][1][2 * hf + 1]));
         mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 1));
-        mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 2));
+        mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 2)) * g.scale_log2;
       }
       const bool up0 = mx[0] > m[mt][0] + kPrRescale, up1 = mx[1] > m[mt][1] + kPrRescale;
       if (__any_sync(0xffffffffu, up0 || up1)) {
@@ -231,7 +231,8 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           const float ref = m[mt][hf] == -INFINITY ? 0.f : m[mt][hf];
-          const float p0 = ex2(sc[mt][n][2 * hf] - ref), p1 = ex2(sc[mt][n][2 * hf + 1] - ref);
+          const float p0 = ex2(fmaf(sc[mt][n][2 * hf], g.scale_log2, -ref));
+          const float p1 = ex2(fmaf(sc[mt][n][2 * hf + 1], g.scale_log2, -ref));
           z[mt][hf] += p0 + p1;
           pa[mt][n * 2 + hf] = pg_pack2<BF>(p0, p1);
         }
