@@ -193,10 +193,16 @@ PROMPTS = [
 ]
 
 
+def wide(H):
+    """Rows to pad a call with so that its bounds send it to the tile kernel, which small ones do not reach."""
+    return 60000 // H
+
+
 @pytest.mark.parametrize("lens,H,Hk,dh,dt,pad", PROMPTS)
-@pytest.mark.parametrize("fused", [False, True])
-def test_prompt_attention(lens, H, Hk, dh, dt, pad, fused):
+@pytest.mark.parametrize("fused,padded", [(False, False), (True, False), (False, True)])
+def test_prompt_attention(lens, H, Hk, dh, dt, pad, fused, padded):
     g = gen(len(lens) * 1000 + H)
+    pad += wide(H) if padded else 0
     cu = starts(lens)
     T = max(1, cu[-1] + pad)
     if fused:
@@ -220,11 +226,12 @@ def test_prompt_attention(lens, H, Hk, dh, dt, pad, fused):
     assert torch.equal(o2, o)  # the same bits without the sums, and on a second call
 
 
-def test_prompt_neighbours_do_not_leak():
+@pytest.mark.parametrize("padded", [0, 1])
+def test_prompt_neighbours_do_not_leak(padded):
     """Infinities and NaN in one request's rows stay in that request."""
     g, lens = gen(5), [200, 77, 300, 131]
     cu = starts(lens)
-    T, H, Hk, dh = cu[-1], 4, 2, 128
+    T, H, Hk, dh = cu[-1] + padded * wide(4), 4, 2, 128
     q, k, v = randn(g, T, H, dh, dtype=BF), randn(g, T, Hk, dh, dtype=BF), randn(g, T, Hk, dh, dtype=BF)
     for x in (q, k, v):
         x[cu[1]:cu[2]] = math.nan
@@ -296,8 +303,11 @@ def workspace(p):
 
 
 @pytest.mark.parametrize("total,new,H,Hk,dh,page,dt,layout,pad", PAGED)
-def test_paged_attention(total, new, H, Hk, dh, page, dt, layout, pad):
-    p, q, kc, vc, table, cu = paged_inputs(total, new, H, Hk, dh, page, dt, layout, pad)
+@pytest.mark.parametrize("padded", [False, True])
+def test_paged_attention(total, new, H, Hk, dh, page, dt, layout, pad, padded):
+    p, q, kc, vc, table, cu = paged_inputs(total, new, H, Hk, dh, page, dt, layout, pad + (wide(H) if padded else 0))
+    if padded:
+        p.max_new = max(p.max_new, 33)
     o, lse, err, ws = torch.full_like(q, 7.0), torch.full((H, q.shape[0]), 7.0, device="cuda"), ints([0]), workspace(p)
     F.flashloop_paged_attn(p, q, kc, vc, table, ints(total), ints(cu), o, lse, ws, err)
     refs = [attention(q[cu[b]:cu[b + 1]], gather(kc, table[b], t), gather(vc, table[b], t), t - new[b], dh ** -0.5) for b, t in enumerate(total)]
@@ -320,10 +330,10 @@ def test_paged_attention_equals_prompt_attention():
     assert ((a[:700].double() - r[0]).abs() <= r[2]).all() and ((a.double() - b.double()).abs()[:700] <= 2 * r[2]).all()
 
 
-@pytest.mark.parametrize("new", [1, 200])
-def test_paged_attention_reports_bad_pages_and_lengths(new):
+@pytest.mark.parametrize("new,padded", [(1, 0), (200, 0), (200, 1)])
+def test_paged_attention_reports_bad_pages_and_lengths(new, padded):
     total = [900, 700, 800]
-    p, q, kc, vc, table, cu = paged_inputs(total, [new] * 3, 4, 2, 128, 16, BF, "thd", 0)
+    p, q, kc, vc, table, cu = paged_inputs(total, [new] * 3, 4, 2, 128, 16, BF, "thd", padded * wide(4))
     table[1, 3], table[2, 5] = p.n_pages, -1
     o, err, ws = torch.full_like(q, 7.0), ints([0]), workspace(p)
     F.flashloop_paged_attn(p, q, kc, vc, table, ints(total), ints(cu), o, None, ws, err)
@@ -360,10 +370,12 @@ def random_paged(seed):
     return total, new, Hk * G, Hk, dh, page, rng.choice((BF, HF)), rng.choice(("thd", "htd", "both")), rng.choice((0, 3))
 
 
-@pytest.mark.parametrize("seed", range(40))
+@pytest.mark.parametrize("seed", range(60))
 def test_paged_attention_over_random_batches(seed):
     total, new, H, Hk, dh, page, dt, layout, pad = random_paged(seed)
-    p, q, kc, vc, table, cu = paged_inputs(total, new, H, Hk, dh, page, dt, layout, pad, seed)
+    p, q, kc, vc, table, cu = paged_inputs(total, new, H, Hk, dh, page, dt, layout, pad + (wide(H) if seed % 2 else 0), seed)
+    if seed % 2:
+        p.max_new = max(p.max_new, 33)
     o, lse, err, ws = torch.full_like(q, 7.0), torch.full((H, q.shape[0]), 7.0, device="cuda"), ints([0]), workspace(p)
     F.flashloop_paged_attn(p, q, kc, vc, table, ints(total), ints(cu), o, lse, ws, err)
     refs = [attention(q[cu[b]:cu[b + 1]], gather(kc, table[b], t), gather(vc, table[b], t), t - new[b], dh ** -0.5) for b, t in enumerate(total)]
@@ -371,14 +383,14 @@ def test_paged_attention_over_random_batches(seed):
     assert err.item() == 0
 
 
-@pytest.mark.parametrize("seed", range(20))
+@pytest.mark.parametrize("seed", range(30))
 def test_prompt_attention_over_random_batches(seed):
     rng = random.Random(1000 + seed)
     Hk, G, dh, dt = rng.choice((1, 2, 5)), rng.choice((1, 2, 3, 7, 8)), rng.choice((64, 128)), rng.choice((BF, HF))
     B = rng.choice((1, 3, 40, 130))
     lens = [rng.choice((0, 1, rng.randint(1, 100), rng.randint(1, 1500 if B < 4 else 300))) for _ in range(B)]
     g, cu, H = gen(seed), starts(lens), Hk * G
-    T = max(1, cu[-1] + rng.choice((0, 9)))
+    T = max(1, cu[-1] + rng.choice((0, 9)) + (wide(H) if seed % 2 else 0))
     q, k, v = randn(g, T, H, dh, dtype=dt, std=2.0), randn(g, T, Hk, dh, dtype=dt), randn(g, T, Hk, dh, dtype=dt)
     o, lse, err = torch.full_like(q, 7.0), torch.full((H, T), 7.0, device="cuda"), ints([0])
     p = F.PagedParams.make(batch=B, max_tokens=T, max_new=max(1, max(lens)), n_heads=H, n_kv_heads=Hk, head_dim=dh, dtype=dt, scale=0.3)
@@ -391,13 +403,14 @@ def test_peaked_and_shifted_scores():
     """Scores hundreds apart, rising along the columns (the running reference is raised again and again), and far from zero."""
     g, n, dh = gen(9), 700, 128
     for rise in (1.0, -1.0):
-        q = torch.ones(n, 2, dh, device="cuda").to(BF)
-        k = (torch.arange(n, device="cuda")[:, None, None] * rise * 0.05 + randn(g, n, 1, dh)).to(BF)
-        v = randn(g, n, 1, dh, dtype=BF)
-        p = F.PagedParams.make(batch=1, max_tokens=n, max_new=n, n_heads=2, n_kv_heads=1, head_dim=dh)
-        o, lse, err = torch.empty(n, 2, dh, dtype=BF, device="cuda"), torch.empty(2, n, device="cuda"), ints([0])
-        F.flashloop_prompt_attn(p, q, k, v, ints([0, n]), o, lse, err)
-        check(o, lse, [0, n], [attention(q, k, v, 0, dh ** -0.5)], True)
+        for T in (n, n + wide(2)):  # few-row and tile kernel
+            q = torch.ones(T, 2, dh, device="cuda").to(BF)
+            k = (torch.arange(T, device="cuda")[:, None, None] * rise * 0.05 + randn(g, T, 1, dh)).to(BF)
+            v = randn(g, T, 1, dh, dtype=BF)
+            p = F.PagedParams.make(batch=1, max_tokens=T, max_new=n, n_heads=2, n_kv_heads=1, head_dim=dh)
+            o, lse, err = torch.full((T, 2, dh), 7.0, dtype=BF, device="cuda"), torch.full((2, T), 7.0, device="cuda"), ints([0])
+            F.flashloop_prompt_attn(p, q, k, v, ints([0, n]), o, lse, err)
+            check(o, lse, [0, n], [attention(q[:n], k[:n], v[:n], 0, dh ** -0.5)], True)
 
 
 def test_equal_keys_average_the_values():
@@ -466,7 +479,7 @@ def test_offsets_beyond_32_bits():
 
 
 def test_two_streams_at_once_and_a_shared_workspace_in_turn():
-    a = paged_inputs([3000, 900, 70], [1, 200, 9], 8, 2, 128, 64, BF, "thd", 0, seed=1)
+    a = paged_inputs([3000, 900, 70], [1, 200, 9], 8, 2, 128, 64, BF, "thd", wide(8), seed=1)
     b = paged_inputs([12000, 40, 5000], [1, 1, 1], 16, 2, 64, 16, HF, "thd", 0, seed=2)
     lens = (ints([3000, 900, 70]), ints([12000, 40, 5000]))
     ws = [workspace(a[0]), workspace(b[0])]
@@ -528,11 +541,11 @@ class Served:
         self.n_free.copy_(self.n_out)
 
 
-@pytest.mark.parametrize("captured", [False, True])
-def test_serving_steps_of_changing_lengths(captured):
+@pytest.mark.parametrize("captured,T", [(False, 320), (True, 320), (True, 7500)])  # the last one's bounds: tile kernel
+def test_serving_steps_of_changing_lengths(captured, T):
     """Chunks, then single tokens, requests joining late: each step's rows attend to all that was written before."""
     H, Hk, dh, page = 8, 2, 64, 16
-    s = Served(B=4, T=320, max_new=200, H=H, Hk=Hk, dh=dh, page=page, n_pages=96, width=32)
+    s = Served(B=4, T=T, max_new=200, H=H, Hk=Hk, dh=dh, page=page, n_pages=96, width=32)
     g, hist = gen(11), [[[], []] for _ in range(4)]
     if captured:
         s.step()  # no new tokens
@@ -542,9 +555,9 @@ def test_serving_steps_of_changing_lengths(captured):
     for new in ([100, 0, 33, 0], [100, 7, 1, 0], [1, 1, 1, 200], [1, 0, 1, 100], [1, 1, 1, 1], [1, 1, 1, 1], [0, 0, 0, 0], [16, 200, 16, 1]):
         n = sum(new)
         s.new.copy_(ints(new))
-        s.q.copy_(randn(g, 320, H, dh, dtype=BF))
-        s.k.copy_(randn(g, 320, Hk, dh))
-        s.v.copy_(randn(g, 320, Hk, dh))
+        s.q.copy_(randn(g, T, H, dh, dtype=BF))
+        s.k.copy_(randn(g, T, Hk, dh))
+        s.v.copy_(randn(g, T, Hk, dh))
         s.o.fill_(7.0)
         graph.replay() if captured else s.step()
         cu = starts(new)
