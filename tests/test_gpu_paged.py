@@ -491,7 +491,7 @@ def test_two_streams_at_once_and_a_shared_workspace_in_turn():
         F.flashloop_paged_attn(p, q, kc, vc, table, kv, ints(cu) if not isinstance(cu, torch.Tensor) else cu, o, None, w, err)
 
     a, b = a[:5] + (ints(a[5]),), b[:5] + (ints(b[5]),)
-    want = [torch.empty_like(a[1]), torch.empty_like(b[1])]
+    want = [torch.zeros_like(a[1]), torch.zeros_like(b[1])]
     run(a, lens[0], ws[0], want[0])
     run(b, lens[1], ws[1], want[1])
     torch.cuda.synchronize()
