@@ -29,7 +29,8 @@
 // prompt of 32768 tokens x 16 heads.
 //
 // Roles (16 warps): 0-3 / 4-7 rows of tile A / B, one thread a row; 8-11
-// queries of the next item; 12 TMEM and K / V loads (lane = page of a tile);
+// queries of the next item and write-back of the last, while the row warps take
+// the next one's exponentials; 12 TMEM and K / V loads (lane = page of a tile);
 // 13 / 14 MMA issue of tile A / B; 15 work items.
 //
 // What bounds it, a pair of 128-column tiles: the MMAs take 2560 cycles (1536
@@ -77,7 +78,8 @@ struct PtCfg {
   static constexpr int kStages = DH == 128 ? 5 : 8;
   static constexpr int kRingOff = 2 * kQBytes;
   static constexpr int kBarOff = kRingOff + kStages * kSlotBytes;
-  static constexpr int kSmem = 1024 + kBarOff + 512;
+  static constexpr int kInvOff = kBarOff + 512;  // 1 / z of both tiles' rows
+  static constexpr int kSmem = 1024 + kInvOff + 2 * kPtRows * 4;
   static_assert(kSmem <= 232448, "shared memory per block");
 };
 
@@ -311,7 +313,8 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   uint64_t* p_full = s_full + 4;             // [x * 2 + half] P of a half written (4 warps)
   uint64_t* pv0_done = p_full + 4;           // [x] the item's last first-half P.V completed
   uint64_t* acc_full = pv0_done + 2;         // [x] the item's last P.V completed
-  uint64_t* n_free = acc_full + 2;           // [x] the numerator has been read (4 warps)
+  uint64_t* inv_full = acc_full + 2;         // [x] the item's 1 / z written (4 warps)
+  uint64_t* n_free = inv_full + 2;           // [x] the numerator has been read (4 warps)
   uint64_t* q_full = n_free + 2;             // [x] queries stored (128 threads)
   uint64_t* q_empty = q_full + 2;            // [x] the item's score MMAs completed
   uint64_t* item_full = q_empty + 2;         // [2]
@@ -320,8 +323,9 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   uint64_t* fin = tail + 1;                  // [1] every MMA of both issuers completed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
   PtItem* items = reinterpret_cast<PtItem*>(tmem_slot + 4);  // [2]
-  static_assert((2 * C::kStages + 24) * 8 + 16 + 2 * sizeof(PtItem) <= 512, "barriers");
+  static_assert((2 * C::kStages + 26) * 8 + 16 + 2 * sizeof(PtItem) <= 512, "barriers");
   uint8_t* ring = smem + C::kRingOff;
+  float* inv_of = reinterpret_cast<float*>(smem + C::kInvOff);  // [x][row]
   const PgArgs& g = a.g;
 
   pg_launch_next();
@@ -338,6 +342,7 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     for (int x = 0; x < 2; ++x) {
       mbar_init(&pv0_done[x], 1);
       mbar_init(&acc_full[x], 1);
+      mbar_init(&inv_full[x], kPtRows / 32);
       mbar_init(&n_free[x], kPtRows / 32);
       mbar_init(&q_full[x], kPtRows);
       mbar_init(&q_empty[x], 1);
@@ -567,8 +572,68 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     // ------------------------------------------------------------ queries
     pt_regs_dec<kPtRegsRest>();
     constexpr int kPieces = DH / 8;
-    PtItem it;
-    for (uint32_t k = 0; next_item(k, it); ++k) {
+    const int quarter = warp - kPtWarpQ, row = quarter * 32 + lane;
+    // The rows of item k, once both tiles' P.V and 1 / z are there: o = N / z, or N to scratch.
+    auto write_back = [&](uint32_t k) -> bool {
+      const PtItem& it = items[k & 1];
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        const int my = pt_mine(it, g, x);
+        const int r = it.r0 + x * kPtRows + row;
+        const bool live = r < it.n * g.G;
+        const int tok = g.by_g(r);
+        uint16_t* od = g.o.p + (live ? (it.q0 + tok) * g.o.st + (long long)(it.h * g.G + r - tok * g.G) * g.o.sh : 0);
+        float4* part = a.part_n + (size_t)it.slot * (DH / 4) * kPtPair + x * kPtRows + row;
+        const bool whole = it.parts == 1;
+        const uint32_t nbase = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(x * DH);
+        if (!wait_warp(&acc_full[x], k & 1) || !wait_warp(&inv_full[x], k & 1)) return false;
+        tc_fence_after();
+        const float inv = inv_of[x * kPtRows + row];
+#pragma unroll 1
+        for (int cc = 0; cc < DH; cc += 16) {
+          uint32_t w[16];
+          if (my > 0) {
+            tmem_ld16(nbase + cc, w);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = 0u;
+          }
+          if (cc + 16 == DH) {  // the numerator is free for the next item's
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&n_free[x]);
+          }
+          if (whole && live) {
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              h[e] = pg_pack2<BF>(__uint_as_float(w[2 * e]) * inv, __uint_as_float(w[2 * e + 1]) * inv);
+            if (g.o32) {
+              st_global_v8(od + cc, h);
+            } else {
+              *reinterpret_cast<uint4*>(od + cc) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(od + cc + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+          } else if (live && my > 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              __stcg(part + (cc / 4 + e) * kPtPair, make_float4(__uint_as_float(w[4 * e]), __uint_as_float(w[4 * e + 1]),
+                                                               __uint_as_float(w[4 * e + 2]), __uint_as_float(w[4 * e + 3])));
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+      return true;
+    };
+    for (uint32_t k = 0;; ++k) {
+      if (!wait_warp(&item_full[k & 1], (k >> 1) & 1)) break;
+      const PtItem& it = items[k & 1];  // kept until its write-back
+      if (!it.valid) {
+        if (k > 0) (void)write_back(k - 1);
+        break;
+      }
       const int rows = it.n * g.G;
       // a warp brings 32 rows of a tile, 16 bytes a lane; lane l knows where row l lies
       auto bring = [&](int x) {
@@ -609,6 +674,7 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       }
       cp_async_wait<0>();
       hand_on(1);
+      if (k > 0 && !write_back(k - 1)) break;
     }
   } else {
     // ------------------------------------------------------------ rows
@@ -720,66 +786,26 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           if (lane == 0) mbar_arrive(&p_full[2 * x + hf]);
         }
       }
-      if (!ok || !wait(&acc_full[x], k & 1)) break;
+      // the write-back is the query warps': the next item's scores are there already.  They have
+      // read the last item's 1 / z when its numerator is free
+      if (!ok || (k > 0 && !wait(&n_free[x], (k - 1) & 1))) break;
       full += my > 0;
       const int r = it.r0 + x * kPtRows + row;
       const bool live = r < it.n * g.G;
-      const int tok = g.by_g(r), hq = it.h * g.G + r - tok * g.G;
-      // write-back; a numerator is read once for all rows of the warp, whether live or not
-      const float inv = z == 0.f ? 0.f : 1.f / z;
-      uint16_t* od = g.o.p + (live ? (it.q0 + tok) * g.o.st + (long long)hq * g.o.sh : 0);
-      auto put = [&](int cc, const float (&v)[32]) {
-        if (!live) return;
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = pg_pack2<BF>(v[2 * e] * inv, v[2 * e + 1] * inv);
-        if (g.o32) {
-          st_global_v8(od + cc, *reinterpret_cast<uint32_t(*)[8]>(&w[0]));
-          st_global_v8(od + cc + 16, *reinterpret_cast<uint32_t(*)[8]>(&w[8]));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(od + cc + 8 * e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-        }
-      };
-      auto put_lse = [&](float m, float zz) {
-        if (live && g.lse)
-          g.lse[(size_t)hq * g.max_tokens + it.q0 + tok] = zz == 0.f ? -INFINITY : (m + log2f(zz)) * kPgLn2;
-      };
-      const size_t prow = (size_t)it.slot * kPtPair + x * kPtRows + row;
-      uint32_t w[2][32];
-      if (my > 0) tmem_ld32(nbase, w[0]);
-#pragma unroll
-      for (int i = 0; i < DH / 32; ++i) {
-        const int cc = 32 * i;
-        float v[32];
-        if (my > 0) {
-          tmem_wait_ld();
-          if (cc + 32 < DH) tmem_ld32(nbase + cc + 32, w[(i + 1) & 1]);
-        }
-        if (cc + 32 == DH) {  // the numerator is free for the next item's
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&n_free[x]);
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = my > 0 ? __uint_as_float(w[i & 1][e]) : 0.f;
-        if (it.parts == 1) {
-          put(cc, v);
-        } else if (live && my > 0) {
-          float4* d = a.part_n + ((size_t)it.slot * (DH / 4) + cc / 4) * kPtPair + x * kPtRows + row;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            __stcg(d + e * kPtPair, make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
+      if (it.parts > 1) {  // a part: another kernel joins them
+        if (live)
+          __stcg(a.part_mz + (size_t)it.slot * kPtPair + x * kPtRows + row,
+                 make_float2(my > 0 ? m_ref : -INFINITY, my > 0 ? z : 0.f));
+      } else {
+        inv_of[x * kPtRows + row] = z == 0.f ? 0.f : 1.f / z;
+        if (live && g.lse) {
+          const int tok = g.by_g(r);
+          g.lse[(size_t)(it.h * g.G + r - tok * g.G) * g.max_tokens + it.q0 + tok] =
+              z == 0.f ? -INFINITY : (m_ref + log2f(z)) * kPgLn2;
         }
       }
-      if (it.parts == 1) {
-        put_lse(m_ref, z);
-        release();
-        continue;
-      }
-      // a part: another kernel joins them
-      if (live) __stcg(a.part_mz + prow, make_float2(my > 0 ? m_ref : -INFINITY, my > 0 ? z : 0.f));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&inv_full[x]);
       release();
     }
   }

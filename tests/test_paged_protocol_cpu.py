@@ -1,8 +1,8 @@
 """Model of pg_tile_kernel's mbarrier protocol (csrc/paged_tile.cu) under random
 schedules: the work-item ring, the K / V slots that both tiles' issuers give
 back, per-half score and P barriers with the next tile's scores issued behind
-each P.V, the wait of a raised reference, the queries' places and the
-numerator's.  Barriers, polls and schedules as in the other kernels' models."""
+each P.V, the wait of a raised reference, the queries' places, and the
+write-back by the query warps while the rows take the next item.  Barriers, polls and schedules as in the other kernels' models."""
 import random
 
 import pytest
@@ -18,7 +18,7 @@ def tile_cta(items, stages, rnd, plant=None):
     for i in range(4):
         B[("s_full", i)], B[("p_full", i)] = Bar(1), Bar(1)  # the four row warps of a tile move together
     for x in range(2):
-        for n in ("pv0_done", "acc_full", "n_free", "q_full", "q_empty", "item_full"):
+        for n in ("pv0_done", "acc_full", "inv_full", "n_free", "q_full", "q_empty", "item_full"):
             B[(n, x)] = Bar(1)
         B[("item_empty", x)] = Bar(6)  # loads, two issuers, queries, two row groups
     B["fin"] = Bar(2)
@@ -102,10 +102,24 @@ def tile_cta(items, stages, rnd, plant=None):
         pipe.append(("commit", "fin"))
         yield from wait(B, "fin", 0)
 
+    held = [-1, -1]  # the item whose 1 / z lies in shared memory
+
     def queries():
+        def write_back(k):
+            for x in range(2):
+                yield from wait(B, ("acc_full", x), k)
+                yield from wait(B, ("inv_full", x), k)
+                assert held[x] == k, "1 / z of another item"
+                for _ in range(rnd.randint(0, 4)):
+                    yield None
+                B[("n_free", x)].arrive()
+            B[("item_empty", k & 1)].arrive()
+
         for k in range(last + 1):
-            yield from item(k)
+            yield from item(k, release=False)
             if k == last:
+                if k > 0:
+                    yield from write_back(k - 1)
                 return
             if k > 0:
                 yield from wait(B, ("q_empty", 0), k - 1)
@@ -118,6 +132,8 @@ def tile_cta(items, stages, rnd, plant=None):
             if both:
                 B[("q_full", 0)].arrive()
             B[("q_full", 1)].arrive()
+            if k > 0:
+                yield from write_back(k - 1)
 
     def rows(x):
         u = full = 0
@@ -141,9 +157,11 @@ def tile_cta(items, stages, rnd, plant=None):
                         yield None
                     B[("p_full", 2 * x + hf)].arrive()
                 u += 1
-            yield from wait(B, ("acc_full", x), k)
             full += my > 0
-            B[("n_free", x)].arrive()
+            if k > 0 and plant != "inv_reuse":
+                yield from wait(B, ("n_free", x), k - 1)
+            held[x] = k
+            B[("inv_full", x)].arrive()
             for _ in range(rnd.randint(0, 3)):
                 yield None
             B[("item_empty", k & 1)].arrive()
@@ -167,7 +185,7 @@ def test_tile_protocol_phases_and_progress(stages):
         tile_cta(random_items(rnd), stages, rnd)
 
 
-@pytest.mark.parametrize("plant", ["kv_empty_count", "p_phase", "pv0_phase"])
+@pytest.mark.parametrize("plant", ["kv_empty_count", "p_phase", "pv0_phase", "inv_reuse"])
 def test_tile_protocol_model_catches_planted_mistakes(plant):
     caught = 0
     for seed in range(30):
