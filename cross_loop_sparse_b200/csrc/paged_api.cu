@@ -19,18 +19,21 @@ static int pg_shift(int page_size) {
   return -1;
 }
 
+// Bounds that leave the kernels' 32-bit sums a tile's or a grid stride's room.
+constexpr long long kPgMaxTokens = 1ll << 30, kPgMaxColumns = 0x7fff0000ll, kPgMaxRows = 0x7fff0000ll;
+
 // Sizes that every call reads.
 static int pg_check_sizes(const flashloop_paged_params* p) {
   if (!p) return FLASHLOOP_ERR_INVALID_ARG;
   if (p->batch < 0 || p->max_tokens < 0 || p->max_new < 1) return FLASHLOOP_ERR_INVALID_ARG;
-  if (p->batch > 65535) return FLASHLOOP_ERR_UNSUPPORTED;
+  if (p->batch > 65535 || p->max_tokens > kPgMaxTokens) return FLASHLOOP_ERR_UNSUPPORTED;
   return FLASHLOOP_OK;
 }
 
 static int pg_check_pages(const flashloop_paged_params* p) {
   if (pg_shift(p->page_size) < 0) return FLASHLOOP_ERR_UNSUPPORTED;
   if (p->n_pages < 1 || p->max_blocks < 1) return FLASHLOOP_ERR_INVALID_ARG;
-  if ((long long)p->n_pages * p->page_size > 0x7fffffffll || (long long)p->max_blocks * p->page_size > 0x7fffffffll)
+  if ((long long)p->n_pages * p->page_size > 0x7fffffffll || (long long)p->max_blocks * p->page_size > kPgMaxColumns)
     return FLASHLOOP_ERR_UNSUPPORTED;
   return FLASHLOOP_OK;
 }
@@ -42,7 +45,7 @@ static int pg_check_heads(const flashloop_paged_params* p, bool queries) {
   if (p->n_kv_heads > 65535) return FLASHLOOP_ERR_UNSUPPORTED;
   if (!queries) return FLASHLOOP_OK;
   if (p->n_heads < 1 || p->n_heads % p->n_kv_heads != 0) return FLASHLOOP_ERR_INVALID_ARG;
-  if ((long long)p->max_tokens * p->n_heads > 0x7fffffffll) return FLASHLOOP_ERR_UNSUPPORTED;  // packed rows are 32-bit
+  if ((long long)p->max_tokens * p->n_heads > kPgMaxRows) return FLASHLOOP_ERR_UNSUPPORTED;  // packed rows
   if (!isfinite(p->scale * kPgLog2e) || !(p->scale > 0.f)) return FLASHLOOP_ERR_INVALID_ARG;
   return FLASHLOOP_OK;
 }

@@ -508,14 +508,15 @@ const char* flashloop_status_string(int status);
 
 typedef struct flashloop_paged_params {
   int32_t batch;      /* B >= 0 requests, at most 65535 */
-  int32_t max_tokens; /* rows of q, o, slot_map and positions (cu[B] may be less) */
+  int32_t max_tokens; /* rows of q, o, slot_map and positions (cu[B] may be less), at most 2^30;
+                       * max_tokens * n_heads at most 2^31 - 2^16 */
   int32_t max_new;    /* bound on the rows of one request, >= 1 */
   int32_t n_heads;    /* query heads, a multiple of n_kv_heads */
   int32_t n_kv_heads;
   int32_t head_dim;   /* 64 or 128 */
   int32_t page_size;  /* 16, 32, 64, 128 or 256 tokens */
   int32_t n_pages;    /* pages of the pool; n_pages * page_size < 2^31 */
-  int32_t max_blocks; /* columns of block_table; max_blocks * page_size < 2^31 */
+  int32_t max_blocks; /* columns of block_table; max_blocks * page_size at most 2^31 - 2^16 */
   int32_t dtype;      /* of q, the cache and o: FLASHLOOP_DTYPE_BF16 or _FP16 */
   float scale;        /* of q.k, > 0, usually 1/sqrt(head_dim) */
 } flashloop_paged_params;
@@ -539,8 +540,8 @@ typedef struct flashloop_pages {
 
 /* Block tables and slot maps from request lengths.  Request b holds kv_lens[b]
  * tokens and appends new_lens[b] >= 0.  free_pages[0..*n_free) is a stack of
- * free pages in a buffer of free_capacity entries; pages are taken from its top, in request order, for the blocks
- * that the new tokens open:
+ * free pages in a buffer of free_capacity entries; pages are taken from its
+ * top, in request order, for the blocks that the new tokens open:
  *   cu[b] = sum of new_lens[0..b) (cu[batch] the total),
  *   kv_lens_out[b] = kv_lens[b] + new_lens[b],
  *   block_table[b, i] for ceil(kv_lens[b]/page_size) <= i < ceil(kv_lens_out[b]/page_size)
@@ -550,9 +551,9 @@ typedef struct flashloop_pages {
  *   *n_free_out = *n_free - pages taken.
  * All or nothing: too few free pages, more than max_tokens tokens or more than
  * max_blocks blocks set FLASHLOOP_DEVERR_CAPACITY, a negative length or a
- * count of free pages outside [0, min(n_pages, free_capacity)] FLASHLOOP_DEVERR_INDEX, and then the
- * call appends nothing: cu is 0, kv_lens_out = kv_lens, *n_free_out = *n_free
- * and every slot -1.  A page id outside [0, n_pages) on the stack or in the
+ * count of free pages outside [0, min(n_pages, free_capacity)]
+ * FLASHLOOP_DEVERR_INDEX, and then the call appends nothing: cu is 0,
+ * kv_lens_out = kv_lens, *n_free_out = *n_free and every slot -1.  A page id outside [0, n_pages) on the stack or in the
  * table sets FLASHLOOP_DEVERR_INDEX and gives its tokens slot -1.  The pages
  * of a finished request go back by writing them at free_pages[*n_free...).
  * kv_lens_out and n_free_out do not overlap the inputs. */

@@ -239,3 +239,24 @@ def test_dealt_list_holds_every_row_pair_once():
             dealt += [r * grid + (grid - 1 - c if r & 1 else c) for c in range(grid)]
             r += 1
         assert sorted(i for i in dealt if i < len(listed)) == list(range(len(listed)))
+
+
+def test_sizes_whose_sums_would_pass_32_bits_are_refused():
+    """Row and column indexes are rounded up to tiles and advanced by strides in 32 bits, so the bounds end below 2^31."""
+    a, B = ctypes.c_void_p(4096), ctypes.byref
+    R, P = B(F.RowsC(4096, 1024, 128)), B(F.PagesC(4096, 65536, 1024, 128))
+
+    def calls(p):
+        yield F._lib.flashloop_paged_plan(B(p), a, a, a, 100, a, a, a, ctypes.c_void_p(8192), a, a, ctypes.c_void_p(12288), a, None)
+        yield F._lib.flashloop_paged_kv_write(B(p), R, R, 0, a, P, P, a, None)
+        yield F._lib.flashloop_prompt_attn(B(p), R, R, R, a, R, None, a, None)
+        yield F._lib.flashloop_paged_attn(B(p), R, P, P, a, a, a, R, None, a, 1 << 62, a, None)
+
+    for big in (2 ** 30 + 1, 2 ** 31 - 1):
+        assert list(calls(params(max_tokens=big, n_heads=2, n_kv_heads=2))) == [-2] * 4, big
+    for big in (2 ** 31 - 2 ** 16 + 1, 2 ** 31 - 1):
+        assert list(calls(params(max_tokens=1, n_heads=big, n_kv_heads=1)))[2:] == [-2] * 2, big
+    for page in (16, 64, 256):
+        rcs = list(calls(params(page_size=page, n_pages=4, max_blocks=(2 ** 31 - 1) // page)))
+        assert [rcs[0], rcs[1], rcs[3]] == [-2] * 3, page
+    assert F.flashloop_paged_attn_workspace_bytes(params(max_blocks=(2 ** 31 - 2 ** 16) // 64)) > 0
