@@ -80,6 +80,11 @@ static bool pg_tma_ok(const PgArgs& g, int pages) {
   return true;
 }
 
+// The tile kernel's roles wait for one another for up to an item's time, and its
+// waits give up after about a second: items of this many columns take 250 ms.
+// The few-row kernel waits for nothing.
+constexpr long long kPgTileColumns = 1ll << 24;
+
 // Which kernel takes a call whose requests see at most `cols` columns, by the
 // call's bounds alone: estimates of both times in microseconds, fitted to both
 // kernels' times over 35 shapes.  A block of the few-row kernel takes a stage of
@@ -94,7 +99,7 @@ static bool pg_tma_ok(const PgArgs& g, int pages) {
 //             63 single rows and one of 64 over 8000 each, 32 heads: 389 / 447
 static bool pg_tiles(const flashloop_paged_params* p, long long cols, bool paged) {
   const long long most = p->max_new < p->max_tokens ? p->max_new : p->max_tokens;
-  if (most * (p->n_heads / p->n_kv_heads) <= kPgFewRows) return false;
+  if (most * (p->n_heads / p->n_kv_heads) <= kPgFewRows || cols > kPgTileColumns) return false;
   auto over = [](double a, double b) { return a > b ? a : b; };
   const double rows = (double)p->max_tokens * p->n_heads;
   const double requests = p->batch < p->max_tokens ? p->batch : p->max_tokens;

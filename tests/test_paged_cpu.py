@@ -260,3 +260,12 @@ def test_sizes_whose_sums_would_pass_32_bits_are_refused():
         rcs = list(calls(params(page_size=page, n_pages=4, max_blocks=(2 ** 31 - 1) // page)))
         assert [rcs[0], rcs[1], rcs[3]] == [-2] * 3, page
     assert F.flashloop_paged_attn_workspace_bytes(params(max_blocks=(2 ** 31 - 2 ** 16) // 64)) > 0
+
+
+def test_items_that_outlast_a_bounded_wait_go_to_the_kernel_without_waits():
+    """The two kernels need scratch of different sizes: 148 x 2 slots of 256 rows, or 296 x 2 of 32."""
+    tile, few = 2 * 148 * 256 * (128 * 4 + 8), 4 * 148 * 32 * (128 * 4 + 8)
+    many = dict(max_tokens=4096, max_new=4096, n_pages=1000)
+    at = F.flashloop_paged_attn_workspace_bytes(params(max_blocks=2 ** 24 // 64, **many))
+    behind = F.flashloop_paged_attn_workspace_bytes(params(max_blocks=2 ** 24 // 64 + 1, **many))
+    assert tile <= at < tile + 2 ** 15 and few <= behind < few + 2 ** 15
