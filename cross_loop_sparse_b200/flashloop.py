@@ -382,7 +382,8 @@ def _rows(fn, name, t, shape, dtype, dev, written=False):
         raise FlashLoopError(fn, -1, f"{name}: head_dim has to be contiguous")
     if written and (st == 0 and shape[0] > 1 or sh == 0 and shape[1] > 1):
         raise FlashLoopError(fn, -1, f"{name}: rows that overlap")
-    return RowsC(t.data_ptr(), st, sh)
+    # a dimension of one may have any stride
+    return RowsC(t.data_ptr(), st if shape[0] > 1 else shape[2], sh if shape[1] > 1 else shape[2])
 
 
 def _pages(fn, name, t, p, dtype, dev, written=False):
@@ -395,7 +396,7 @@ def _pages(fn, name, t, p, dtype, dev, written=False):
         raise FlashLoopError(fn, -1, f"{name}: head_dim has to be contiguous")
     if written and (sp == 0 and shape[0] > 1 or st == 0 or sh == 0 and shape[2] > 1):
         raise FlashLoopError(fn, -1, f"{name}: pages that overlap")
-    return PagesC(t.data_ptr(), sp, st, sh)
+    return PagesC(t.data_ptr(), sp if shape[0] > 1 else shape[3], st, sh if shape[2] > 1 else shape[3])
 
 
 def _paged_dtype(fn, p):

@@ -269,3 +269,16 @@ def test_items_that_outlast_a_bounded_wait_go_to_the_kernel_without_waits():
     at = F.flashloop_paged_attn_workspace_bytes(params(max_blocks=2 ** 24 // 64, **many))
     behind = F.flashloop_paged_attn_workspace_bytes(params(max_blocks=2 ** 24 // 64 + 1, **many))
     assert tile <= at < tile + 2 ** 15 and few <= behind < few + 2 ** 15
+
+
+def test_strides_of_single_entries_do_not_matter():
+    """torch may give a dimension of one any stride; the library asks for multiples of 16 bytes."""
+    bf = torch.bfloat16
+    t = torch.empty(4096, dtype=bf)
+    for st, sh in ((1, 128), (1, 3), (256, 5), (0, 0)):
+        shape = (1, 2 if sh == 128 else 1, 128)
+        r = F._rows("f", "q", t.as_strided(shape, (st, sh, 1)), shape, bf, -1, written=True)
+        assert r.stride_token % 8 == 0 and r.stride_head % 8 == 0 and r.stride_token > 0 and r.stride_head > 0
+    p = F.PagedParams.make(1, 1, 1, 1, 1, 128, page_size=16, n_pages=1)
+    c = F._pages("f", "k_cache", t.as_strided((1, 16, 1, 128), (3, 128, 5, 1)), p, bf, -1, written=True)
+    assert (c.stride_page % 8, c.stride_token, c.stride_head % 8) == (0, 128, 0)
