@@ -41,10 +41,10 @@
 // of them against 1166 without, alone, and a slower kernel).
 //
 // Work: without scratch (prompts) an item is a whole row pair, dealt to and fro
-// from a list that begins with the longest.  With scratch (paged) the column tiles of all items are one
-// line that is cut into equal lengths, one a block, so that few rows over a
-// long cache still use every SM; an item cut by a border leaves float32 N, m
-// and z in scratch, which another kernel joins.
+// from a list that begins with the longest.  With scratch (paged) the column
+// tiles of all items are one line that is cut into equal lengths, one a block,
+// so that few rows over a long cache still use every SM; an item cut by a
+// border leaves float32 N, m and z in scratch, which another kernel joins.
 //
 // Every wait is bounded; one that gives up sets FLASHLOOP_DEVERR_TIMEOUT, and the
 // block unwinds.
@@ -569,7 +569,7 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       (void)mbar_wait(fin, 0);
     }
   } else if (warp >= kPtWarpQ) {
-    // ------------------------------------------------------------ queries
+    // ------------------------------------------------------------ queries and write-back
     pt_regs_dec<kPtRegsRest>();
     constexpr int kPieces = DH / 8;
     const int quarter = warp - kPtWarpQ, row = quarter * 32 + lane;
