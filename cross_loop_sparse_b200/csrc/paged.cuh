@@ -85,6 +85,11 @@ __device__ __forceinline__ uint32_t pg_pack2(float lo, float hi) {
   return pack_half2(lo, hi);
 }
 template <int BF>
+__device__ __forceinline__ float2 pg_unpack2(uint32_t x) {
+  if (BF) return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&x));
+  return __half22float2(*reinterpret_cast<__half2*>(&x));
+}
+template <int BF>
 __device__ __forceinline__ void pg_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if (BF) mma_bf16(d, a, b0, b1);
   else mma_f16(d, a, b0, b1);

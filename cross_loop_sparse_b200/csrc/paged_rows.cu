@@ -11,11 +11,15 @@
 // the end.  With m the running reference (log2 units, raised only when a
 // score exceeds it by 8, which bounds a probability by 2^8),
 //   p = 2^(s - m), z = sum p, N = sum p v, o = N / z, lse = (m + log2 z) ln 2.
-// Scores, sums and N are float32; p is rounded to the values' type, since the
-// matrix product takes one type.
+// Scores, sums and N are float32.  The matrix product takes p in the values'
+// type.  Up to 16 packed rows, what that rounding drops is multiplied with V too,
+// so that the rounding of o alone is left: up to 8 rows in the places of rows 8
+// to 15, at no cost, up to 16 in products of their own (16 contexts of 16384
+// tokens, 16 heads a key head: 95 to 98 us).  With more rows, whose products
+// bound the kernel, p is rounded, which makes the error sqrt(2) times as large.
 //
 // Bound by HBM: a column costs 4 * head_dim bytes and few instructions (8 contexts
-// of 32768 tokens, 16 heads of 128: 316 to 329 us, 6.5 to 6.8 TB/s; with 17 to 32
+// of 32768 tokens, 16 heads of 128: 318 to 329 us, 6.5 to 6.8 TB/s; with 17 to 32
 // packed rows 4.4 TB/s, where eight warps an SM cannot hide two tiles' products).  With
 // scratch, the stages of all requests and key heads are one line that is cut
 // into equal lengths, one a block and two blocks an SM, so that requests of any
@@ -62,10 +66,13 @@ struct PrItem {
   int slot, parts;  // scratch slot, number of parts of the whole item (1 = this is all)
 };
 
-template <int DH, int BF, int MT>
+// LO: what the rounding of p to the values' type drops goes through the product
+// with V too, in the place of rows 8 to 15 (1) or in a product of its own (2).
+template <int DH, int BF, int MT, int LO>
 __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_t* smem) {
   using C = PrCfg<DH, MT>;
   constexpr int kPieces = DH / 8;
+  constexpr int kHalves = LO == 1 ? 1 : 2;  // eights of rows that a tile's are
   const PgArgs& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = s.b, h = s.h, r0 = s.r0;
@@ -159,14 +166,14 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
 #pragma unroll
   for (int i = 0; i < C::kStages; ++i) load(i);
 
-  float o[MT][DH / 8][4];
+  float o[MT][DH / 8][4], ol[MT][LO == 2 ? DH / 8 : 1][4];
   float m[MT][2], z[MT][2];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
     for (int n = 0; n < DH / 8; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+      for (int e = 0; e < 4; ++e) o[mt][n][e] = ol[mt][LO == 2 ? n : 0][e] = 0.f;
     m[mt][0] = m[mt][1] = -INFINITY;
     z[mt][0] = z[mt][1] = 0.f;
   }
@@ -194,28 +201,29 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
         pg_mma<BF>(sc[mt][1], qa[mt][ks], kb[2], kb[3]);
       }
     }
-    uint32_t pa[MT][4];
+    uint32_t pa[MT][4], lo[MT][4];
     if (c0 + 16 > free_cols) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
+          for (int e = 0; e < 2 * kHalves; ++e)
             if (c0 + n * 8 + (lane & 3) * 2 + (e & 1) > lim[mt][e >> 1]) sc[mt][n][e] = -INFINITY;
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      float mx[2];
+      float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+      for (int hf = 0; hf < kHalves; ++hf) {
         mx[hf] = fmaxf(fmaxf(sc[mt][0][2 * hf], sc[mt][0][2 * hf + 1]), fmaxf(sc[mt][1][2 * hf], sc[mt][1][2 * hf + 1]));
         mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 1));
         mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 2)) * g.scale_log2;
       }
       const bool up0 = mx[0] > m[mt][0] + kPrRescale, up1 = mx[1] > m[mt][1] + kPrRescale;
       if (__any_sync(0xffffffffu, up0 || up1)) {
-        const float f0 = up0 ? ex2(m[mt][0] - mx[0]) : 1.f, f1 = up1 ? ex2(m[mt][1] - mx[1]) : 1.f;
+        const float f0 = up0 ? ex2(m[mt][0] - mx[0]) : 1.f;
+        const float f1 = LO == 1 ? f0 : up1 ? ex2(m[mt][1] - mx[1]) : 1.f;
         if (up0) m[mt][0] = mx[0];
         if (up1) m[mt][1] = mx[1];
         z[mt][0] *= f0;
@@ -226,17 +234,27 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
           o[mt][n][1] *= f0;
           o[mt][n][2] *= f1;
           o[mt][n][3] *= f1;
+          if (LO == 2) {
+            ol[mt][n][0] *= f0;
+            ol[mt][n][1] *= f0;
+            ol[mt][n][2] *= f1;
+            ol[mt][n][3] *= f1;
+          }
         }
       }
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
+        for (int hf = 0; hf < kHalves; ++hf) {
           const float ref = m[mt][hf] == -INFINITY ? 0.f : m[mt][hf];
           const float p0 = ex2(fmaf(sc[mt][n][2 * hf], g.scale_log2, -ref));
           const float p1 = ex2(fmaf(sc[mt][n][2 * hf + 1], g.scale_log2, -ref));
           z[mt][hf] += p0 + p1;
           pa[mt][n * 2 + hf] = pg_pack2<BF>(p0, p1);
+          if (LO) {
+            const float2 h = pg_unpack2<BF>(pa[mt][n * 2 + hf]);
+            (LO == 1 ? pa[mt][n * 2 + 1] : lo[mt][n * 2 + hf]) = pg_pack2<BF>(p0 - h.x, p1 - h.y);
+          }
         }
     }
 #pragma unroll
@@ -249,6 +267,10 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
       for (int mt = 0; mt < MT; ++mt) {
         pg_mma<BF>(o[mt][2 * n2], pa[mt], vb[0], vb[1]);
         pg_mma<BF>(o[mt][2 * n2 + 1], pa[mt], vb[2], vb[3]);
+        if (LO == 2) {
+          pg_mma<BF>(ol[mt][2 * n2], lo[mt], vb[0], vb[1]);
+          pg_mma<BF>(ol[mt][2 * n2 + 1], lo[mt], vb[2], vb[3]);
+        }
       }
     }
     __syncwarp();
@@ -264,7 +286,7 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
+    for (int hf = 0; hf < kHalves; ++hf) {
       float zz = z[mt][hf];
       zz += __shfl_xor_sync(0xffffffffu, zz, 1);
       zz += __shfl_xor_sync(0xffffffffu, zz, 2);
@@ -276,7 +298,15 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
       float* d = so + (warp * C::kRows + r) * C::kPitch + (lane & 3) * 2;
 #pragma unroll
       for (int n = 0; n < DH / 8; ++n)
-        *reinterpret_cast<float2*>(d + n * 8) = make_float2(o[mt][n][2 * hf], o[mt][n][2 * hf + 1]);
+      {
+        float2 x = make_float2(o[mt][n][2 * hf], o[mt][n][2 * hf + 1]);
+        if (LO) {  // an infinite value gives an infinite product with p, and one of any sign, or none, with the rest
+          const float2 l = LO == 1 ? make_float2(o[mt][n][2], o[mt][n][3]) : make_float2(ol[mt][n][2 * hf], ol[mt][n][2 * hf + 1]);
+          if (isfinite(l.x)) x.x += l.x;
+          if (isfinite(l.y)) x.y += l.y;
+        }
+        *reinterpret_cast<float2*>(d + n * 8) = x;
+      }
     }
   __syncthreads();
   for (int i = threadIdx.x; i < C::kRows * (DH / 4); i += kPrThreads) {
@@ -321,6 +351,15 @@ __device__ __forceinline__ int pr_tiles(const PgArgs& g, const PgSeq& s) {
   return (s.n * g.G + kPgFewRows - 1) / kPgFewRows;
 }
 
+// By the rows of the request: up to 16 do half of a 32-row tile's products.
+template <int DH, int BF, int MT>
+__device__ __forceinline__ void pr_one(const PrArgs& a, const PrItem& it, uint8_t* smem) {
+  const int rows = it.n * a.g.G;
+  if (rows <= 8) pr_item<DH, BF, 1, 1>(a, it, smem);
+  else if (MT == 1 || rows <= 16) pr_item<DH, BF, 1, 2>(a, it, smem);
+  else pr_item<DH, BF, MT, 0>(a, it, smem);
+}
+
 template <int DH, int BF, int MT>
 __global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PrArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -334,7 +373,7 @@ __global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PrArgs a) {
     if (r0 >= rows) return;
     const int seen = q.L - q.n + g.by_g(min(rows, r0 + PrCfg<DH, MT>::kRows) - 1) + 1;  // by the tile's last row
     PrItem it{(int)blockIdx.z, (int)blockIdx.y, q.q0, q.n, q.L, r0, 0, max(0, seen), 0, 1};
-    pr_item<DH, BF, MT>(a, it, smem);
+    pr_one<DH, BF, MT>(a, it, smem);
     return;
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -415,9 +454,7 @@ __global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PrArgs a) {
       it.slot = blockIdx.x * 2 + (fc == blockIdx.x && s0 != fc * per);
       if (it.parts > 1 && fc == blockIdx.x && tid == 0)
         a.cuts[blockIdx.x] = PgCut{it.parts, it.slot, it.h, it.q0, it.n, it.r0, {0, 0}};
-      // a request of one row tile does half of the products
-      if (MT == 2 && q.n * g.G <= 16) pr_item<DH, BF, 1>(a, it, smem);
-      else pr_item<DH, BF, MT>(a, it, smem);
+      pr_one<DH, BF, MT>(a, it, smem);
       __syncthreads();  // shared memory goes to the next item
       x = end;
     }

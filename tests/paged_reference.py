@@ -20,10 +20,10 @@ def build_plan(held, new, table, stack, page):
     return cu, kv, table, slots, pos, len(stack)
 
 
-def attention(q, k, v, first, scale):
+def attention(q, k, v, first, scale, p_parts=1):
     """q [n, H, dh], k and v [L, Hk, dh]; row i sees the columns j <= first + i.  Returns o, lse and
     the elementwise bounds of a kernel that takes scores and sums in float32 and rounds the
-    probabilities and the output to q's type."""
+    probabilities (to a sum of p_parts numbers) and the output to q's type."""
     n, H, dh = q.shape
     L, G = k.shape[0], H // k.shape[1]
     u = torch.finfo(q.dtype).eps / 2
@@ -51,7 +51,8 @@ def attention(q, k, v, first, scale):
         o[:, h] = p @ vz
         # half a step of p and of o; fp16 also has an absolute step of 2^-25 below 2^-14 (p and o)
         flat = 2.0 ** -25 if q.dtype == torch.float16 else 0.0
-        o_tol[:, h] = u * 1.01 * (a + o[:, h].abs() + rel[:, None] * a) + rel[:, None] * a \
+        # (of two parts the second is at most half a step, and off by half a step of its own)
+        o_tol[:, h] = u * 1.01 * (u ** (p_parts - 1) * a + o[:, h].abs() + rel[:, None] * a) + rel[:, None] * a \
             + flat * (1 + vz.abs().sum(0))[None] + 1e-30
         lse[h] = l
         lse_tol[h] = ds + 2.0 ** -21 + (L + 16) * 2.0 ** -24 + 4 * 2.0 ** -24 * (mag + 20)

@@ -660,3 +660,30 @@ def test_binding_refusals():
             prompt(params=bad)
         assert e.value.status == status
     assert (o == 7).all() and err.item() == 0
+
+
+SMALL = [  # cached lengths, new tokens, H, Hk, dh, type: up to 16 packed rows a request and key head
+    ([1, 77, 400], [1, 1, 1], 1, 1, 64, BF), ([3000, 5, 64], [1, 1, 1], 8, 1, 128, BF), ([5000, 9], [2, 1], 8, 2, 128, HF), ([2100, 65], [1, 1], 12, 1, 64, HF),
+    ([4096, 300], [4, 3], 8, 2, 128, BF), ([450, 16], [2, 2], 7, 1, 64, BF), ([900] * 40, [1] * 40, 16, 1, 128, HF), ([700, 3000], [1, 16], 4, 4, 128, BF),
+]
+
+
+@pytest.mark.parametrize("total,new,H,Hk,dh,dt", SMALL)
+def test_few_rows_keep_what_the_rounding_of_p_drops(total, new, H, Hk, dh, dt):
+    p, q, kc, vc, table, cu = paged_inputs(total, new, H, Hk, dh, 16, dt, "thd", 0)
+    o, err = torch.full_like(q, 7.0), ints([0])
+    F.flashloop_paged_attn(p, q, kc, vc, table, ints(total), ints(cu), o, None, workspace(p), err)
+    refs = [attention(q[cu[b]:cu[b + 1]], gather(kc, table[b], t), gather(vc, table[b], t), t - new[b], dh ** -0.5, 2) for b, t in enumerate(total)]
+    check(o, None, cu, refs, False)
+
+
+@pytest.mark.parametrize("G,dt", [(4, BF), (8, HF), (12, BF), (16, HF), (24, BF)])
+@pytest.mark.parametrize("L", [40, 2000])
+def test_infinite_values_stay_infinite(G, dt, L):
+    """Seen by every row: an infinity of V is the result's, one of either sign none's."""
+    p, q, kc, vc, table, cu = paged_inputs([L], [1], G, 1, 64, 16, dt, "thd", 0)
+    vc[table[0, 1].long(), 3, 0, :2], vc[table[0, 0].long(), 9, 0, 1] = math.inf, -math.inf
+    vc[table[0, 0].long(), 0, 0, 2] = math.nan
+    o = torch.zeros_like(q)
+    F.flashloop_paged_attn(p, q, kc, vc, table, ints([L]), ints(cu), o, None, workspace(p), ints([0]))
+    assert (o[..., 0] == math.inf).all() and o[..., 1:3].isnan().all() and o[..., 3:].isfinite().all()
