@@ -1,4 +1,5 @@
-"""Build the sm_100a shared library libflashloop.so in place (nvcc, no GPU needed).
+"""Build the sm_100a shared library libflashloop.so in place (nvcc, no GPU needed),
+and the marshalling of the many-request calls, _fastcall.so (g++).
 
 Usage: python -m cross_loop_sparse_b200.build [-v] [--force]
 """
@@ -8,6 +9,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libflashloop.so")
+FAST = os.path.join(PKG, "_fastcall.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -53,12 +56,34 @@ def _compile(src: str, verbose: bool, force: bool) -> str:
     return obj
 
 
+def _build_fastcall(force: bool) -> None:
+    src = os.path.join(CSRC, "fastcall.cpp")
+    newest_dep = max(os.path.getmtime(f) for f in [src, os.path.join(INCLUDE, "flashloop.h")])
+    if not force and os.path.exists(FAST) and os.path.getmtime(FAST) >= newest_dep:
+        return
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE]
+    for inc in (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include")):
+        cmd += ["-isystem", inc]
+    tmp = FAST + ".tmp"
+    cmd += [src, "-o", tmp, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, FAST)
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
-    """Compile every csrc/*.cu for sm_100a and link libflashloop.so; returns its path."""
+    """Compile every csrc/*.cu for sm_100a and link libflashloop.so, and build _fastcall.so; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        fast = ex.submit(_build_fastcall, force)
         objs = list(ex.map(lambda s: _compile(s, verbose, force), srcs))
+        fast.result()
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         tmp = LIB + ".tmp"
         cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs

@@ -405,6 +405,22 @@ def _paged_dtype(fn, p):
     return torch.float16 if p.dtype else torch.bfloat16
 
 
+# The same marshalling in C++ for the plain case, tensors on the current device; None where it leaves
+# a call to the functions below.
+try:
+    from . import _fastcall
+except ImportError as exc:
+    raise ImportError(f"{_PKG}/_fastcall.so: build it with `python -m cross_loop_sparse_b200.build`") from exc
+_fastcall.bind(*(ctypes.cast(getattr(_lib, fn), c_void_p).value for fn in (
+    "flashloop_paged_plan", "flashloop_paged_kv_write", "flashloop_prompt_attn", "flashloop_paged_attn")))
+
+
+def _done(fn, rc):
+    if rc:
+        raise FlashLoopError(fn, rc)
+    return rc
+
+
 # The current stream's handle without a Stream object (a microsecond less a call) where torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -418,9 +434,7 @@ def _launch(fn, dev, stream, *args):
             rc = getattr(_lib, fn)(*args, _stream(stream))
     else:
         rc = getattr(_lib, fn)(*args, _raw_stream(dev) if stream is None and _raw_stream else _stream(stream))
-    if rc:
-        raise FlashLoopError(fn, rc)
-    return rc
+    return _done(fn, rc)
 
 
 def flashloop_paged_plan(params, kv_lens, new_lens, free_pages, n_free, block_table, cu, kv_lens_out, slot_map,
@@ -428,6 +442,10 @@ def flashloop_paged_plan(params, kv_lens, new_lens, free_pages, n_free, block_ta
     """Block tables, slot maps, positions and packed starts of the tokens that the requests
     append (see the header).  int32 tensors; block_table [batch, max_blocks] and n_free_out,
     kv_lens_out, cu [batch + 1], slot_map and positions [max_tokens] are written."""
+    rc = _fastcall.plan(params, kv_lens, new_lens, free_pages, n_free, block_table, cu, kv_lens_out, slot_map, positions,
+                        n_free_out, err_word, stream)
+    if rc is not None:
+        return _done("flashloop_paged_plan", rc)
     fn, p, dev, i32 = "flashloop_paged_plan", params, kv_lens.get_device(), torch.int32
     B, T = max(p.batch, 0), max(p.max_tokens, 0)
     return _launch(fn, dev, stream, ctypes.byref(p), _vec(fn, "kv_lens", kv_lens, B, i32, dev),
@@ -442,6 +460,9 @@ def flashloop_paged_plan(params, kv_lens, new_lens, free_pages, n_free, block_ta
 def flashloop_paged_kv_write(params, k, v, slot_map, k_cache, v_cache, err_word, stream=None):
     """Write k and v [max_tokens, n_kv_heads, head_dim] (params.dtype or float32) into the pages
     [n_pages, page_size, n_kv_heads, head_dim] of their slots."""
+    rc = _fastcall.write(params, k, v, slot_map, k_cache, v_cache, err_word, stream)
+    if rc is not None:
+        return _done("flashloop_paged_kv_write", rc)
     fn, p, dev = "flashloop_paged_kv_write", params, k_cache.get_device()
     dt = _paged_dtype(fn, p)
     shape = (p.max_tokens, p.n_kv_heads, p.head_dim)
@@ -457,6 +478,9 @@ def flashloop_paged_kv_write(params, k, v, slot_map, k_cache, v_cache, err_word,
 def flashloop_prompt_attn(params, q, k, v, cu, o, lse, err_word, stream=None):
     """Causal attention over packed prompts: q and o [max_tokens, n_heads, head_dim], k and v
     [max_tokens, n_kv_heads, head_dim], cu int32 [batch + 1], lse float32 [n_heads, max_tokens] or None."""
+    rc = _fastcall.prompt(params, q, k, v, cu, o, lse, err_word, stream)
+    if rc is not None:
+        return _done("flashloop_prompt_attn", rc)
     fn, p, dev = "flashloop_prompt_attn", params, q.get_device()
     dt = _paged_dtype(fn, p)
     qs, ks = (p.max_tokens, p.n_heads, p.head_dim), (p.max_tokens, p.n_kv_heads, p.head_dim)
@@ -476,6 +500,9 @@ def flashloop_paged_attn(params, q, k_cache, v_cache, block_table, kv_lens, cu, 
                          stream=None):
     """Attention of the requests' new rows q [max_tokens, n_heads, head_dim] over their pages
     (block_table int32 [batch, max_blocks], kv_lens int32 [batch] with the new tokens counted)."""
+    rc = _fastcall.attn(params, q, k_cache, v_cache, block_table, kv_lens, cu, o, lse, workspace, err_word, stream)
+    if rc is not None:
+        return _done("flashloop_paged_attn", rc)
     fn, p, dev = "flashloop_paged_attn", params, q.get_device()
     dt = _paged_dtype(fn, p)
     qs = (p.max_tokens, p.n_heads, p.head_dim)
