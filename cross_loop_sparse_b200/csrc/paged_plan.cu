@@ -42,6 +42,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs g) {
   __shared__ unsigned long long s_new, s_opened;
   __shared__ int s_bad;
   const int tid = threadIdx.x;
+  pg_wait_for_launch_before();
+  pg_launch_next();
   if (tid == 0) {
     s_new = s_opened = 0;
     s_bad = 0;
@@ -158,8 +160,7 @@ int launch_paged_plan(const flashloop_paged_params* p, int shift, const int32_t*
   int grid = (p->max_tokens + kPlanTokens - 1) / kPlanTokens;
   if (grid > 148) grid = 148;
   if (grid < 1) grid = 1;
-  paged_plan_kernel<<<grid, kPlanThreads, 0, stream>>>(g);
-  return launch_status();
+  return pg_launch_early(paged_plan_kernel, dim3(grid), kPlanThreads, 0, stream, g);
 }
 
 // ---------------------------------------------------------------------------
@@ -203,6 +204,8 @@ __global__ void __launch_bounds__(256) paged_kv_write_kernel(WriteArgs g) {
   const long long total = (long long)g.T * per_token;
   const long long slots = (long long)g.n_pages << g.shift;
   bool range = false;
+  pg_wait_for_launch_before();
+  pg_launch_next();
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
     const int t = (int)(i / per_token), r = (int)(i - (long long)t * per_token);
     const int h = r / kPieces, c = (r % kPieces) * 8;
@@ -235,17 +238,13 @@ int launch_paged_kv_write(const flashloop_paged_params* p, int shift, const flas
   long long blocks = (total + 255) / 256;
   const int grid = (int)(blocks > 148 * 16 ? 148 * 16 : blocks);
   const int bf = p->dtype == FLASHLOOP_DTYPE_BF16;
-  auto go = [&](auto kernel) { kernel<<<grid, 256, 0, stream>>>(g); };
+  auto go = [&](auto kernel) { return pg_launch_early(kernel, dim3(grid), 256, 0, stream, g); };
   if (p->head_dim == 128) {
-    if (!src32) go(paged_kv_write_kernel<128, 0, 1>);
-    else if (bf) go(paged_kv_write_kernel<128, 1, 1>);
-    else go(paged_kv_write_kernel<128, 1, 0>);
-  } else {
-    if (!src32) go(paged_kv_write_kernel<64, 0, 1>);
-    else if (bf) go(paged_kv_write_kernel<64, 1, 1>);
-    else go(paged_kv_write_kernel<64, 1, 0>);
+    if (!src32) return go(paged_kv_write_kernel<128, 0, 1>);
+    return bf ? go(paged_kv_write_kernel<128, 1, 1>) : go(paged_kv_write_kernel<128, 1, 0>);
   }
-  return launch_status();
+  if (!src32) return go(paged_kv_write_kernel<64, 0, 1>);
+  return bf ? go(paged_kv_write_kernel<64, 1, 1>) : go(paged_kv_write_kernel<64, 1, 0>);
 }
 
 }  // namespace fl

@@ -365,6 +365,7 @@ __global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PrArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_b;
   __shared__ long long s_sum[kPrThreads / 32], s_at;
+  pg_wait_for_launch_before();
   pg_launch_next();
   const PgArgs& g = a.g;
   if (a.cuts == nullptr) {
@@ -470,8 +471,7 @@ int launch_pg_rows(const PgArgs& g, int dh, int bf16, const PgScratch& ws, cudaS
     FL_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     dim3 grid((unsigned)((rows + rt - 1) / rt), g.Hk, g.B);
     if (a.cuts) grid = dim3(2 * kPgSms);  // each leaves a record
-    kernel<<<grid, kPrThreads, smem, stream>>>(a);
-    return launch_status();
+    return pg_launch_early(kernel, grid, kPrThreads, smem, stream, a);
   };
   auto pick = [&](auto dhc) -> int {
     constexpr int DH = decltype(dhc)::value;

@@ -328,7 +328,6 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   float* inv_of = reinterpret_cast<float*>(smem + C::kInvOff);  // [x][row]
   const PgArgs& g = a.g;
 
-  pg_launch_next();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -357,6 +356,8 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  pg_wait_for_launch_before();
+  pg_launch_next();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -868,8 +869,7 @@ int launch_pg_tile(const PgArgs& g, int dh, int bf16, const PgScratch& ws, cudaS
   }
   auto go = [&](auto kernel, int smem) -> int {
     FL_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    kernel<<<grid, kPtThreads, smem, stream>>>(tk, tv, a);
-    return launch_status();
+    return pg_launch_early(kernel, dim3(grid), kPtThreads, smem, stream, tk, tv, a);
   };
   if (dh == 128) {
     if (bf16) return go(pg_tile_kernel<128, 1>, PtCfg<128>::kSmem);

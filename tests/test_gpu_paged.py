@@ -687,3 +687,57 @@ def test_infinite_values_stay_infinite(G, dt, L):
     o = torch.zeros_like(q)
     F.flashloop_paged_attn(p, q, kc, vc, table, ints([L]), ints(cu), o, None, workspace(p), ints([0]))
     assert (o[..., 0] == math.inf).all() and o[..., 1:3].isnan().all() and o[..., 3:].isfinite().all()
+
+
+@pytest.mark.parametrize("mode", ["eager", "captured", "streams"])
+@pytest.mark.parametrize("n", [2, 300])  # few-row kernel, tile kernel
+def test_calls_back_to_back_see_each_other(mode, n):
+    """Each call reads what the one before it wrote, and writes what the one before it read; nothing waits on the host.
+    The same bits as with a wait after every call."""
+    B, H, Hk, dh, page, steps = 3, 8, 2, 64, 16, 12
+    width = steps * n // page + 2
+    p = F.PagedParams.make(batch=B, max_tokens=B * n, max_new=n, n_heads=H, n_kv_heads=Hk, head_dim=dh, page_size=page, n_pages=B * width, max_blocks=width)
+    q0 = randn(gen(3), B * n, H, dh, dtype=BF)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+
+    def run(mode):
+        q, o, ws, err = q0.clone(), torch.zeros_like(q0), workspace(p), ints([0])
+        kv, new, free, left = [ints([0] * B), ints([0] * B)], ints([n] * B), ints(list(range(B * width))), [ints([B * width]), ints([0])]
+        table, cu, slots, pos = torch.full((B, width), -1, dtype=torch.int32, device="cuda"), ints([0] * (B + 1)), ints([0] * B * n), ints([0] * B * n)
+        kc, vc = (torch.full((B * width, page, Hk, dh), math.nan, dtype=BF, device="cuda") for _ in range(2))
+        torch.cuda.synchronize()
+
+        def calls():
+            for i in range(steps):
+                a, b = i % 2, (i + 1) % 2
+                yield lambda: F.flashloop_paged_plan(p, kv[a], new, free, left[a], table, cu, kv[b], slots, pos, left[b], err)
+                yield lambda: F.flashloop_paged_kv_write(p, q[:, :Hk], q[:, Hk:2 * Hk], slots, kc, vc, err)
+                yield lambda: F.flashloop_paged_attn(p, q, kc, vc, table, kv[b], cu, o, None, ws, err)
+                yield lambda: F.flashloop_prompt_attn(p, o, o[:, 2:4], q[:, 4:6], cu, q, None, err) if i % 3 == 2 else q.copy_(o)
+                yield lambda: F.flashloop_prompt_attn(p, q, o[:, 2:4], o[:, 4:6], cu, q, None, err)
+
+        if mode == "captured":
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                for call in calls():
+                    call()
+            graph.replay()
+        else:
+            for i, call in enumerate(calls()):
+                if mode == "streams":
+                    here, there = streams[i % 2], streams[(i + 1) % 2]
+                    here.wait_stream(there)
+                    with torch.cuda.stream(here):
+                        call()
+                else:
+                    call()
+                if mode == "waits":
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert err.item() == 0
+        return q, o, kc[free.new_tensor(table[:, :steps * n // page].flatten().tolist()).long()]
+
+    want = run("waits")
+    assert want[0].isfinite().all() and want[0].abs().sum() > 0
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(run(mode), want))
