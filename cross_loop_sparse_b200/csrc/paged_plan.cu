@@ -5,7 +5,8 @@
 // launch and two or three dependent L2 reads, so one launch does all: every
 // block repeats the scan over the requests (a few KB out of L2) and then takes
 // its share of the tokens, which needs no exchange between blocks.  64 requests
-// of a token each take 3.8 us, 512 with 250 thousand tokens 6.8 us (in a graph).
+// of a token each take 3.3 us, 512 with 250 thousand tokens 5.8 us in a graph
+// (half as many blocks 7.8, twice as many 7.7).
 //
 // write: a copy with a gathered destination, bound by HBM.  A thread moves one
 // 16-byte piece of a row's K and of its V, so both loads are in flight at once:
@@ -36,25 +37,48 @@ __device__ __forceinline__ int plan_blocks(int len, int shift) {
   return (int)(((long long)len + (1 << shift) - 1) >> shift);
 }
 
+// Exclusive sums over the block of two counts at once, both below 2^31: (tokens, pages), and over all of it.
+__device__ __forceinline__ int2 plan_scan(int tokens, int pages, unsigned long long (&s_warp)[kPlanThreads / 32], int2& all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned long long mine = (unsigned long long)pages << 32 | (unsigned)tokens;
+  unsigned long long sum = mine, before = 0, total = 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += y;
+  }
+  if (lane == 31) s_warp[warp] = sum;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w == warp) before = total;
+    total += s_warp[w];
+  }
+  before += sum - mine;
+  all = make_int2((int)(unsigned)total, (int)(total >> 32));
+  return make_int2((int)(unsigned)before, (int)(before >> 32));
+}
+
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs g) {
   __shared__ int s_start[kPlanThreads], s_open[kPlanThreads], s_kv[kPlanThreads];
-  __shared__ int s_scan[32];
-  __shared__ unsigned long long s_new, s_opened;
-  __shared__ int s_bad;
+  __shared__ unsigned long long s_warp[kPlanThreads / 32];
+  __shared__ ulonglong2 s_sums[kPlanThreads / 32];  // tokens and pages of a warp's requests
+  __shared__ int s_bad[kPlanThreads / 32];
   const int tid = threadIdx.x;
   pg_wait_for_launch_before();
   pg_launch_next();
-  if (tid == 0) {
-    s_new = s_opened = 0;
-    s_bad = 0;
-  }
-  __syncthreads();
+  const int n_free = *g.n_free;
+  int kv0 = 0, n0 = 0;  // of the first chunk's request
   // totals first: the call appends everything or nothing
+  unsigned long long tn = 0, to = 0;
+  int bad = 0;
   {
-    unsigned long long tn = 0, to = 0;
-    int bad = 0;
     for (int b = tid; b < g.B; b += kPlanThreads) {
       const int kv = g.kv[b], n = g.add[b];
+      if (b == tid) {
+        kv0 = kv;
+        n0 = n;
+      }
       if (kv < 0 || n < 0) {
         bad |= FLASHLOOP_DEVERR_INDEX;
         continue;
@@ -64,29 +88,36 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs g) {
       tn += n;
       to += end - plan_blocks(kv, g.shift);
     }
+    auto sum = [&](int lanes) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      tn += __shfl_xor_sync(0xffffffffu, tn, o);
-      to += __shfl_xor_sync(0xffffffffu, to, o);
-      bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+      for (int o = lanes / 2; o > 0; o >>= 1) {
+        tn += __shfl_xor_sync(0xffffffffu, tn, o);
+        to += __shfl_xor_sync(0xffffffffu, to, o);
+        bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+      }
+    };
+    const int warp = tid >> 5, lane = tid & 31;
+    sum(32);
+    if (lane == 0) {
+      s_sums[warp] = make_ulonglong2(tn, to);
+      s_bad[warp] = bad;
     }
-    if ((tid & 31) == 0) {
-      atomicAdd(&s_new, tn);
-      atomicAdd(&s_opened, to);
-      if (bad) atomicOr(&s_bad, bad);
-    }
+    __syncthreads();
+    const int from = lane % (kPlanThreads / 32);
+    tn = s_sums[from].x;
+    to = s_sums[from].y;
+    bad = s_bad[from];
+    sum(kPlanThreads / 32);
   }
-  __syncthreads();
-  const int n_free = *g.n_free;
   int code = 0;
-  if ((s_bad & FLASHLOOP_DEVERR_INDEX) || n_free < 0 || n_free > g.max_free) code = FLASHLOOP_DEVERR_INDEX;
-  else if (s_bad || s_new > (unsigned long long)g.T || s_opened > (unsigned long long)n_free)
+  if ((bad & FLASHLOOP_DEVERR_INDEX) || n_free < 0 || n_free > g.max_free) code = FLASHLOOP_DEVERR_INDEX;
+  else if (bad || tn > (unsigned long long)g.T || to > (unsigned long long)n_free)
     code = FLASHLOOP_DEVERR_CAPACITY;
-  const int total = code ? 0 : (int)s_new;
+  const int total = code ? 0 : (int)tn;
   if (blockIdx.x == 0 && tid == 0) {
     if (code) set_error(g.err, code);
     g.cu[g.B] = total;
-    *g.n_free_out = code ? n_free : n_free - (int)s_opened;
+    *g.n_free_out = code ? n_free : n_free - (int)to;
   }
   const int share = (g.T + gridDim.x - 1) / gridDim.x;
   const int t0 = min(g.T, (int)min((long long)blockIdx.x * share, (long long)g.T)), t1 = min(g.T, t0 + share);
@@ -105,23 +136,23 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs g) {
   int base = 0, opened = 0;  // of the requests before this chunk
   for (int b0 = 0; b0 < g.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
-    const int kv = b < g.B ? g.kv[b] : 0, n = b < g.B ? g.add[b] : 0;
+    const int kv = b0 == 0 ? kv0 : b < g.B ? g.kv[b] : 0, n = b0 == 0 ? n0 : b < g.B ? g.add[b] : 0;
     const int old = plan_blocks(kv, g.shift);
     const int open = plan_blocks(kv + n, g.shift) - old;
-    int chunk_new, chunk_open;
-    const int start = base + block_exclusive_scan(n, s_scan, &chunk_new);
-    const int first = opened + block_exclusive_scan(open, s_scan, &chunk_open);
+    int2 chunk;
+    const int2 before = plan_scan(n, open, s_warp, chunk);
+    const int start = base + before.x;
     s_start[tid] = start;
-    s_open[tid] = first - old;  // block i of the request takes stack entry n_free - 1 - (this + i)
+    s_open[tid] = opened + before.y - old;  // block i of the request takes stack entry n_free - 1 - (this + i)
     s_kv[tid] = kv;
     if (blockIdx.x == 0 && b < g.B) {
       g.cu[b] = start;
       g.kv_out[b] = kv + n;
     }
     __syncthreads();
-    const int end = min(t1, base + chunk_new);
+    const int end = min(t1, base + chunk.x);
     for (int t = max(t0, base) + tid; t < end; t += kPlanThreads) {
-      int lo = 0, hi = kPlanThreads;  // last request of the chunk that starts at or before t
+      int lo = 0, hi = min(kPlanThreads, g.B - b0);  // last request of the chunk that starts at or before t
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (s_start[mid] <= t) lo = mid;
@@ -142,8 +173,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs g) {
       g.slot[t] = good ? (page << g.shift) + in : -1;
       g.pos[t] = pos;
     }
-    base += chunk_new;
-    opened += chunk_open;
+    base += chunk.x;
+    opened += chunk.y;
     __syncthreads();
     // the other blocks only need the requests of their own tokens
     if (blockIdx.x != 0 && base >= t1) break;
