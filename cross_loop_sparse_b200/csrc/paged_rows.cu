@@ -354,7 +354,8 @@ __device__ __forceinline__ int pr_tiles(const PgArgs& g, const PgSeq& s) {
   return (s.n * g.G + kPgFewRows - 1) / kPgFewRows;
 }
 
-// By the rows of the request: up to 16 do half of a 32-row tile's products.
+// By the rows of the request: up to 16 do half of a 32-row tile's products.  The kernel of 16-row
+// tiles takes requests of any number of rows.
 template <int DH, int BF, int MT>
 __device__ __forceinline__ void pr_one(const PrArgs& a, const PrItem& it, uint8_t* smem) {
   const int rows = it.n * a.g.G;
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PrArgs a) {
   const PgArgs& g = a.g;
   if (a.cuts == nullptr) {
     const PgSeq q = pg_seq(g, blockIdx.z);
-    const int rows = q.n * g.G, r0 = blockIdx.x * PrCfg<DH, MT>::kRows;
+    const int rows = q.n * g.G, r0 = (gridDim.x - 1 - blockIdx.x) * PrCfg<DH, MT>::kRows;  // long ones first
     if (r0 >= rows) return;
     const int seen = q.L - q.n + g.by_g(min(rows, r0 + PrCfg<DH, MT>::kRows) - 1) + 1;  // by the tile's last row
     PrItem it{(int)blockIdx.z, (int)blockIdx.y, q.q0, q.n, q.L, r0, 0, max(0, seen), 0, 1};
@@ -470,6 +471,11 @@ __global__ void __launch_bounds__(kPrThreads) pg_rows_kernel(PrArgs a) {
 int launch_pg_rows(const PgArgs& g, int dh, int bf16, const PgScratch& ws, cudaStream_t stream) {
   PrArgs a{g, ws.row_cuts, ws.row_mz, ws.row_n};
   const long long rows = (long long)g.max_new * g.G;
+  // Whole tiles of 16 rows if every SM gets one at most: a stage of 16 is shorter (4 prompts of 100
+  // tokens, 4 heads of 128: 5.0 us against 7.9), but two blocks of 16 on an SM take longer than one
+  // of 32 (16 of 128 tokens, 4 heads of 64: 8.3 against 6.2).
+  const long long tiles16 = (long long)g.max_tokens * g.Hq / 16 + (long long)(g.B < g.max_tokens ? g.B : g.max_tokens) * g.Hk / 2;
+  const bool narrow = rows <= 16 || (!a.cuts && tiles16 <= kPgSms);
   auto go = [&](auto kernel, int rt, int smem) -> int {
     FL_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     dim3 grid((unsigned)((rows + rt - 1) / rt), g.Hk, g.B);
@@ -478,7 +484,7 @@ int launch_pg_rows(const PgArgs& g, int dh, int bf16, const PgScratch& ws, cudaS
   };
   auto pick = [&](auto dhc) -> int {
     constexpr int DH = decltype(dhc)::value;
-    if (rows <= 16) {
+    if (narrow) {
       if (bf16) return go(pg_rows_kernel<DH, 1, 1>, 16, PrCfg<DH, 1>::kSmem);
       return go(pg_rows_kernel<DH, 0, 1>, 16, PrCfg<DH, 1>::kSmem);
     }

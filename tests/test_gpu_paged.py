@@ -741,3 +741,16 @@ def test_calls_back_to_back_see_each_other(mode, n):
     assert want[0].isfinite().all() and want[0].abs().sum() > 0
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(run(mode), want))
+
+
+@pytest.mark.parametrize("lens,H,Hk,dh,dt", [([100] * 4, 4, 4, 128, BF), ([17], 4, 4, 64, HF), ([33, 1, 80], 6, 2, 64, BF), ([300, 41], 4, 1, 128, HF), ([1024], 2, 2, 64, BF)])
+def test_small_prompts_in_tiles_of_16_rows(lens, H, Hk, dh, dt):
+    """At most a tile an SM: every tile of every request, whose probabilities keep what their rounding drops."""
+    g, cu = gen(sum(lens)), starts(lens)
+    q, k, v = randn(g, cu[-1], H, dh, dtype=dt, std=1.5), randn(g, cu[-1], Hk, dh, dtype=dt), randn(g, cu[-1], Hk, dh, dtype=dt)
+    p = F.PagedParams.make(batch=len(lens), max_tokens=cu[-1], max_new=max(lens), n_heads=H, n_kv_heads=Hk, head_dim=dh, dtype=dt)
+    assert cu[-1] * H // 16 + len(lens) * Hk // 2 <= 148
+    o, lse, err = torch.full_like(q, 7.0), torch.full((H, cu[-1]), 7.0, device="cuda"), ints([0])
+    F.flashloop_prompt_attn(p, q, k, v, ints(cu), o, lse, err)
+    check(o, lse, cu, [attention(q[a:b], k[a:b], v[a:b], 0, dh ** -0.5, 2) for a, b in zip(cu, cu[1:])], True)
+    assert err.item() == 0
