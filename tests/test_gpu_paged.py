@@ -754,3 +754,36 @@ def test_small_prompts_in_tiles_of_16_rows(lens, H, Hk, dh, dt):
     F.flashloop_prompt_attn(p, q, k, v, ints(cu), o, lse, err)
     check(o, lse, cu, [attention(q[a:b], k[a:b], v[a:b], 0, dh ** -0.5, 2) for a, b in zip(cu, cu[1:])], True)
     assert err.item() == 0
+
+
+def test_both_ways_into_the_library(monkeypatch):
+    """The C++ marshalling takes plain calls, and gives what the Python one does; that refuses the same calls."""
+    s = [Served(B=2, T=24, max_new=16, H=4, Hk=2, dh=64, page=16, n_pages=12, width=4) for _ in range(2)]
+    g = gen(21)
+    x = [randn(g, 24, h, 64) for h in (4, 2, 2)]
+    for c in s:
+        c.new.copy_(ints([16, 5]))
+        for to, a in zip((c.q, c.k, c.v), x):
+            to.copy_(a)
+
+    def calls(c):
+        o = torch.full_like(c.q, 7.0)
+        yield "plan", (c.p, c.kv, c.new, c.free, c.n_free, c.table, c.cu, c.kv_out, c.slots, c.pos, c.n_out, c.err)
+        yield "write", (c.p, c.k, c.v, c.slots, c.kc, c.vc, c.err)
+        yield "attn", (c.p, c.q, c.kc, c.vc, c.table, c.kv_out, c.cu, c.o, None, c.ws, c.err)
+        yield "prompt", (c.p, c.q, c.k.to(BF), c.v.to(BF), c.cu, o, None, c.err)
+        c.o2 = o
+
+    public = dict(plan=F.flashloop_paged_plan, write=F.flashloop_paged_kv_write, attn=F.flashloop_paged_attn, prompt=F.flashloop_prompt_attn)
+    for name, args in calls(s[0]):
+        assert getattr(F._fastcall, name)(*args, None) == 0
+    here = torch.cuda.current_stream()
+    for name, args in calls(s[1]):
+        assert getattr(F._fastcall, name)(*args, here) is None  # a stream object: the Python path's
+        assert getattr(F._fastcall, name)(*args[:-1], args[-1].cpu(), None) is None
+        assert public[name](*args, stream=here) == 0
+    for a, b in ((s[0].o, s[1].o), (s[0].o2, s[1].o2), (s[0].table, s[1].table), (s[0].slots, s[1].slots), (s[0].kv_out, s[1].kv_out), (s[0].n_out, s[1].n_out)):
+        assert torch.equal(a, b)
+    assert torch.equal(torch.nan_to_num(s[0].kc), torch.nan_to_num(s[1].kc)) and s[0].err.item() == s[1].err.item() == 0
+    monkeypatch.setattr(F, "_fastcall", type("Without", (), {n: staticmethod(lambda *a: None) for n in public}))
+    test_binding_refusals()
