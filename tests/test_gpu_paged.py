@@ -787,3 +787,27 @@ def test_both_ways_into_the_library(monkeypatch):
     assert torch.equal(torch.nan_to_num(s[0].kc), torch.nan_to_num(s[1].kc)) and s[0].err.item() == s[1].err.item() == 0
     monkeypatch.setattr(F, "_fastcall", type("Without", (), {n: staticmethod(lambda *a: None) for n in public}))
     test_binding_refusals()
+
+
+@pytest.mark.parametrize("width,most", [(2, 1), (40, 1), (40, 90)])  # few-row kernel whole and cut, tile kernel
+def test_the_largest_batch(width, most):
+    B, H, Hk, dh, page = 65535, 4, 1, 64, 16
+    rng = np.random.default_rng(most * width)
+    new = rng.integers(0, 2, B)
+    if most > 1:
+        new[rng.integers(0, B, 40)] = most
+    total = new + rng.integers(0, page * 2 - 1 if width == 2 else 60, B) if most == 1 else np.maximum(new, rng.integers(0, 100, B))
+    total = np.minimum(total, page * width)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    T, n_pages = int(cu[-1]), 5000
+    g = gen(width)
+    table = torch.randint(0, n_pages, (B, width), generator=g, device="cuda", dtype=torch.int32)  # pages shared at random
+    kc, vc, q = randn(g, n_pages, page, Hk, dh, dtype=BF), randn(g, n_pages, page, Hk, dh, dtype=BF), randn(g, T, H, dh, dtype=BF)
+    p = F.PagedParams.make(batch=B, max_tokens=T, max_new=most, n_heads=H, n_kv_heads=Hk, head_dim=dh, page_size=page, n_pages=n_pages, max_blocks=width)
+    o, err = torch.full_like(q, 7.0), ints([0])
+    F.flashloop_paged_attn(p, q, kc, vc, table, ints(total.tolist()), ints(cu.tolist()), o, None, workspace(p), err)
+    assert err.item() == 0 and not (o == 7.0).all(-1).any()
+    for b in [0, 1, B - 2, B - 1] + rng.integers(0, B, 40).tolist() + np.argsort(new)[-10:].tolist():
+        t, n, r = int(total[b]), int(new[b]), slice(int(cu[b]), int(cu[b + 1]))
+        want, _, tol, _ = attention(q[r], gather(kc, table[b], t), gather(vc, table[b], t), t - n, dh ** -0.5)
+        assert ((o[r].double() - want).abs() <= tol).all(), b
