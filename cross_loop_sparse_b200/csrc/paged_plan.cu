@@ -209,12 +209,14 @@ struct WriteArgs {
   int32_t* err;
 };
 
-// Eight elements as 16-bit words: a copy, or float32 rounded to nearest even.
+// Eight elements as 16-bit words: a copy, or float32 rounded to nearest even.  Read once, through
+// coherent loads: the kernel in front may still be writing the rows when this one starts, and a
+// load of the read-only path could move before the wait for its end.
 template <int SRC32, int BF>
 __device__ __forceinline__ uint4 write_load(const void* base, long long off, bool& range) {
-  if (!SRC32) return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off));
+  if (!SRC32) return __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off));
   const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off);
-  const float4 a = __ldg(s), b = __ldg(s + 1);
+  const float4 a = __ldcs(s), b = __ldcs(s + 1);
   if (!BF) {
     const float m = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
                           fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
