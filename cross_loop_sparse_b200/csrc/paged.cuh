@@ -95,6 +95,32 @@ __device__ __forceinline__ void pg_mma(float (&d)[4], const uint32_t (&a)[4], ui
   else mma_f16(d, a, b0, b1);
 }
 
+// Values that are not finite.  A row's probability of a column that it does not see is zero, and zero
+// times infinity or NaN would reach the row through the product.  So the values of columns that some
+// row of a tile does not see are looked over before the product; those that are not finite are zero
+// in it, and are added to the numerators of the rows that see them beside it.
+//
+// pg_finite_fma(x, 0 or an earlier result): zeros, or not once a value of the pair was not finite.
+template <int BF>
+__device__ __forceinline__ uint32_t pg_finite_fma(uint32_t x, uint32_t acc) {
+  if (BF) {
+    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&x), __float2bfloat162_rn(0.f), *reinterpret_cast<__nv_bfloat162*>(&acc));
+    return *reinterpret_cast<const uint32_t*>(&r) & 0x7fff7fffu;
+  }
+  const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&x), __float2half2_rn(0.f), *reinterpret_cast<__half2*>(&acc));
+  return *reinterpret_cast<const uint32_t*>(&r) & 0x7fff7fffu;
+}
+template <int BF>
+__device__ __forceinline__ bool pg_not_finite(uint32_t bits) {  // of one value
+  constexpr uint32_t kExp = BF ? 0x7f80u : 0x7c00u;
+  return (bits & kExp) == kExp;
+}
+// The pair with zeros for what is not finite.
+template <int BF>
+__device__ __forceinline__ uint32_t pg_finite_part(uint32_t x) {
+  return (pg_not_finite<BF>(x) ? 0u : x & 0xffffu) | (pg_not_finite<BF>(x >> 16) ? 0u : x & 0xffff0000u);
+}
+
 // The scratch of the paged attention.  A block that takes a cut of the column
 // line holds at most two items that are not whole, the first and the last, and
 // at most one whose part 0 it has; of that one it leaves a record.

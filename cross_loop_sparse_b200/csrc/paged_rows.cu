@@ -185,7 +185,7 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
     cp_async_wait<C::kStages - 1>();
     __syncwarp();
     const uint8_t* kt = ring + (st % C::kStages) * 2 * C::kTile;
-    const uint8_t* vt = kt + C::kTile;
+    uint8_t* vt = ring + (st % C::kStages) * 2 * C::kTile + C::kTile;
     const int c0 = s.c0 + st * kPrCols + warp * 16;
     float sc[MT][2][4];
 #pragma unroll
@@ -205,6 +205,7 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
       }
     }
     uint32_t pa[MT][4], lo[MT][4];
+    bool odd = false;  // a value that is not finite in a column that some row does not see
     if (c0 + 16 > free_cols) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -213,6 +214,12 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
 #pragma unroll
           for (int e = 0; e < 2 * kHalves; ++e)
             if (c0 + n * 8 + (lane & 3) * 2 + (e & 1) > lim[mt][e >> 1]) sc[mt][n][e] = -INFINITY;
+      uint32_t f = 0;  // columns from ncols on are zeros
+      for (int i = max(0, free_cols - c0) * kPieces + lane; i < min(16, ncols - c0) * kPieces; i += 32) {
+        const uint4 x = *reinterpret_cast<const uint4*>(vt + i * 16);
+        f = pg_finite_fma<BF>(x.w, pg_finite_fma<BF>(x.z, pg_finite_fma<BF>(x.y, pg_finite_fma<BF>(x.x, f))));
+      }
+      odd = __any_sync(0xffffffffu, f != 0);
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -259,6 +266,30 @@ __device__ __forceinline__ void pr_item(const PrArgs& a, const PrItem& s, uint8_
             (LO == 1 ? pa[mt][n * 2 + 1] : lo[mt][n * 2 + hf]) = pg_pack2<BF>(p0 - h.x, p1 - h.y);
           }
         }
+    }
+    if (odd) {
+#pragma unroll 1
+      for (int j = max(0, free_cols - c0); j < 16; ++j) {
+#pragma unroll
+        for (int n = 0; n < DH / 8; ++n) {
+          uint32_t* at = reinterpret_cast<uint32_t*>(vt + j * DH * 2 + ((n ^ (j & 7)) << 4)) + (lane & 3);
+          const uint32_t x = *at, rest = pg_finite_part<BF>(x);
+          if (x != rest) {
+            const float2 add = pg_unpack2<BF>(x ^ rest);  // a zero beside a value that is not finite stays one
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int hf = 0; hf < kHalves; ++hf)
+                if (c0 + j <= lim[mt][hf]) {
+                  o[mt][n][2 * hf] += add.x;
+                  o[mt][n][2 * hf + 1] += add.y;
+                }
+          }
+          __syncwarp();
+          *at = rest;
+        }
+      }
+      __syncwarp();
     }
 #pragma unroll
     for (int n2 = 0; n2 < DH / 16; ++n2) {
