@@ -214,9 +214,9 @@ struct WriteArgs {
 // load of the read-only path could move before the wait for its end.
 template <int SRC32, int BF>
 __device__ __forceinline__ uint4 write_load(const void* base, long long off, bool& range) {
-  if (!SRC32) return __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off));
+  if (!SRC32) return *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off);
   const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off);
-  const float4 a = __ldcs(s), b = __ldcs(s + 1);
+  const float4 a = s[0], b = s[1];
   if (!BF) {
     const float m = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
                           fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
