@@ -100,16 +100,6 @@ __device__ __forceinline__ void pg_mma(float (&d)[4], const uint32_t (&a)[4], ui
 // row of a tile does not see are looked over before the product; those that are not finite are zero
 // in it, and are added to the numerators of the rows that see them beside it.
 //
-// pg_finite_fma(x, 0 or an earlier result): zeros, or not once a value of the pair was not finite.
-template <int BF>
-__device__ __forceinline__ uint32_t pg_finite_fma(uint32_t x, uint32_t acc) {
-  if (BF) {
-    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&x), __float2bfloat162_rn(0.f), *reinterpret_cast<__nv_bfloat162*>(&acc));
-    return *reinterpret_cast<const uint32_t*>(&r) & 0x7fff7fffu;
-  }
-  const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&x), __float2half2_rn(0.f), *reinterpret_cast<__half2*>(&acc));
-  return *reinterpret_cast<const uint32_t*>(&r) & 0x7fff7fffu;
-}
 template <int BF>
 __device__ __forceinline__ bool pg_not_finite(uint32_t bits) {  // of one value
   constexpr uint32_t kExp = BF ? 0x7f80u : 0x7c00u;

@@ -109,3 +109,4 @@ FEW_PAGED = [  # whole requests up to 512 columns, cut lines beyond; 8, 16 and m
 @pytest.mark.parametrize("total,new,H,Hk,dh,page,dt,layout", FEW_PAGED)
 def test_paged_rows_see_their_own_columns_values(total, new, H, Hk, dh, page, dt, layout):
     paged_case(total, new, H, Hk, dh, page, dt, layout, 0, False)
+
