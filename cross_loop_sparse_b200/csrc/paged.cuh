@@ -96,10 +96,31 @@ __device__ __forceinline__ void pg_mma(float (&d)[4], const uint32_t (&a)[4], ui
 }
 
 // Values that are not finite.  A row's probability of a column that it does not see is zero, and zero
-// times infinity or NaN would reach the row through the product.  So the values of columns that some
-// row of a tile does not see are looked over before the product; those that are not finite are zero
-// in it, and are added to the numerators of the rows that see them beside it.
+// times infinity or NaN would reach the row through the product.  So the values that are not finite
+// of columns that some row of a tile does not see are zeros in the product, and are added to the
+// numerators of the rows that see them.
 //
+// Looks over pairs of values: x * 0 is zero, or NaN for what is not finite.  Four sums, so that a
+// 16-byte piece's products do not wait for one another.
+template <int BF>
+struct PgFinite {
+  uint32_t sum[4] = {0u, 0u, 0u, 0u};
+  static __device__ __forceinline__ uint32_t fma0(uint32_t x, uint32_t acc) {
+    if (BF) {
+      const __nv_bfloat162 r = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&x), __float2bfloat162_rn(0.f), *reinterpret_cast<__nv_bfloat162*>(&acc));
+      return *reinterpret_cast<const uint32_t*>(&r);
+    }
+    const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&x), __float2half2_rn(0.f), *reinterpret_cast<__half2*>(&acc));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  __device__ __forceinline__ void add(const uint4& x) {
+    sum[0] = fma0(x.x, sum[0]);
+    sum[1] = fma0(x.y, sum[1]);
+    sum[2] = fma0(x.z, sum[2]);
+    sum[3] = fma0(x.w, sum[3]);
+  }
+  __device__ __forceinline__ bool all() const { return ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) == 0; }
+};
 template <int BF>
 __device__ __forceinline__ bool pg_not_finite(uint32_t bits) {  // of one value
   constexpr uint32_t kExp = BF ? 0x7f80u : 0x7c00u;

@@ -499,9 +499,9 @@ const char* flashloop_status_string(int status);
  * count as zero).  Memory behind a request's last cached token is not used,
  * whatever bits it holds.
  *
- * Keys and values that are not finite: a row's result depends on those of the
- * columns it may see; within a tile of 128 columns a value (not a key) that is
- * not finite can also reach rows of the same request before it. */
+ * Keys and values that are not finite reach the rows that see their column, and
+ * no others.  An infinite value is the row's result there, or NaN beside one of the
+ * other sign; with a probability too small for the values' type it may be either. */
 #define FLASHLOOP_DTYPE_BF16 0
 #define FLASHLOOP_DTYPE_FP16 1
 #define FLASHLOOP_DTYPE_FP32 2

@@ -110,3 +110,23 @@ FEW_PAGED = [  # whole requests up to 512 columns, cut lines beyond; 8, 16 and m
 def test_paged_rows_see_their_own_columns_values(total, new, H, Hk, dh, page, dt, layout):
     paged_case(total, new, H, Hk, dh, page, dt, layout, 0, False)
 
+
+TILE_PROMPTS = [
+    ([200, 1, 77, 640], 4, 2, 128, BF), ([1500], 2, 2, 64, HF), ([300, 129, 128, 1000], 8, 8, 128, HF), ([90, 257, 31], 16, 1, 64, BF), ([130, 70], 40, 2, 128, BF),
+]
+
+
+@pytest.mark.parametrize("lens,H,Hk,dh,dt", TILE_PROMPTS)
+def test_prompt_tiles_see_their_own_columns_values(lens, H, Hk, dh, dt):
+    prompt_case(lens, H, Hk, dh, dt, wide(H), True)
+
+
+TILE_PAGED = [
+    ([2000, 333, 900], [300, 40, 128], 4, 2, 128, 16, BF, "thd"), ([700, 130, 64], [700, 100, 64], 4, 4, 64, 128, HF, "htd"), ([9000, 50, 400], [513, 50, 1], 8, 1, 128, 256, BF, "both"),
+    ([300, 700, 1000], [400, 37, 999], 6, 2, 128, 32, HF, "thd"),
+]
+
+
+@pytest.mark.parametrize("total,new,H,Hk,dh,page,dt,layout", TILE_PAGED)
+def test_paged_tiles_see_their_own_columns_values(total, new, H, Hk, dh, page, dt, layout):
+    paged_case(total, new, H, Hk, dh, page, dt, layout, wide(H), True)
