@@ -66,8 +66,21 @@ struct Call {
     return t.data_ptr();
   }
   int32_t* ints(PyObject* o, long long n) const { return static_cast<int32_t*>(vec(o, n, at::kInt)); }
-  float* floats_or_none(PyObject* o, long long n) const {
-    return o == Py_None ? nullptr : static_cast<float*>(vec(o, n, at::kFloat));
+
+  // The same in rows of `row` elements: flat, or its last dimensions make up a row.
+  void* in_rows(PyObject* o, long long n, long long row, at::ScalarType of) const {
+    const at::Tensor& t = tensor(o);
+    long long size = 1;
+    int64_t d = t.dim();
+    while (size != row && d > 0) size *= t.size(--d);
+    if (n > 0 && size != row && t.dim() > 1) throw NotPlain();
+    return vec(o, n, of);
+  }
+  int32_t* table(PyObject* o) const {
+    return static_cast<int32_t*>(in_rows(o, (long long)p.batch * p.max_blocks, p.max_blocks, at::kInt));
+  }
+  float* lse(PyObject* o) const {
+    return o == Py_None ? nullptr : static_cast<float*>(in_rows(o, (long long)p.max_tokens * p.n_heads, p.max_tokens, at::kFloat));
   }
 
   // [tokens, heads, head_dim]; a dimension of one may have any stride.
@@ -121,7 +134,7 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t *kv = c.ints(a[1], B), *add = c.ints(a[2], B), *stack = c.ints(a[3], 0), *n_free = c.ints(a[4], 1);
     const long long capacity = Call::tensor(a[3]).numel();
     if (capacity > 0x7fffffffll) throw NotPlain();
-    int32_t *table = c.ints(a[5], B * c.p.max_blocks), *cu = c.ints(a[6], B + 1), *kv_out = c.ints(a[7], B);
+    int32_t *table = c.table(a[5]), *cu = c.ints(a[6], B + 1), *kv_out = c.ints(a[7], B);
     int32_t *slot = c.ints(a[8], T), *pos = c.ints(a[9], T), *left = c.ints(a[10], 1), *err = c.ints(a[11], 1);
     return without_gil([&] {
       return plan_fn(&c.p, kv, add, stack, (int32_t)capacity, n_free, table, cu, kv_out, slot, pos, left, err, c.stream);
@@ -146,11 +159,10 @@ PyObject* kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return run(n, 9, [&] {
     const Call c(a[0], a[1], a[8]);
-    const long long T = c.p.max_tokens;
     const flashloop_rows q = c.rows(a[1], c.p.n_heads, c.type), k = c.rows(a[2], c.p.n_kv_heads, c.type);
     const flashloop_rows v = c.rows(a[3], c.p.n_kv_heads, c.type), o = c.rows(a[5], c.p.n_heads, c.type, true);
     const int32_t* cu = c.ints(a[4], c.p.batch + 1ll);
-    float* lse = c.floats_or_none(a[6], T * c.p.n_heads);
+    float* lse = c.lse(a[6]);
     int32_t* err = c.ints(a[7], 1);
     return without_gil([&] { return prompt_fn(&c.p, &q, &k, &v, cu, &o, lse, err, c.stream); });
   });
@@ -159,11 +171,11 @@ PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return run(n, 12, [&] {
     const Call c(a[0], a[1], a[11]);
-    const long long B = c.p.batch, T = c.p.max_tokens;
+    const long long B = c.p.batch;
     const flashloop_rows q = c.rows(a[1], c.p.n_heads, c.type), o = c.rows(a[7], c.p.n_heads, c.type, true);
     const flashloop_pages kc = c.pages(a[2]), vc = c.pages(a[3]);
-    const int32_t *table = c.ints(a[4], B * c.p.max_blocks), *kv = c.ints(a[5], B), *cu = c.ints(a[6], B + 1);
-    float* lse = c.floats_or_none(a[8], T * c.p.n_heads);
+    const int32_t *table = c.table(a[4]), *kv = c.ints(a[5], B), *cu = c.ints(a[6], B + 1);
+    float* lse = c.lse(a[8]);
     const at::Tensor& ws = Call::tensor(a[9]);
     if (!ws.is_cuda() || ws.get_device() != c.dev || !ws.is_contiguous()) throw NotPlain();
     void* scratch = ws.data_ptr();

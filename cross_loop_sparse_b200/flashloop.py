@@ -365,12 +365,22 @@ def flashloop_check_error_word(err_word, stream=None):
 
 
 # ----------------------------------------------------------------------------- many requests
-def _vec(fn, name, t, n, dtype, dev):
-    """Address of a contiguous vector of at least n elements on CUDA device dev (an index)."""
-    if t.dtype is dtype and t.get_device() == dev and t.numel() >= n and t.is_contiguous():
+def _in_rows(shape, row):
+    """Whether a contiguous tensor is rows of `row` elements: flat, or its last dimensions make up a row."""
+    size = 1
+    for d in reversed(shape):
+        if size == row:
+            return True
+        size *= d
+    return size == row or len(shape) < 2
+
+
+def _vec(fn, name, t, n, dtype, dev, row=1):
+    """Address of a contiguous vector of at least n elements, in rows of `row`, on CUDA device dev (an index)."""
+    if t.dtype is dtype and t.get_device() == dev and t.numel() >= n and t.is_contiguous() and (row == 1 or n == 0 or _in_rows(t.shape, row)):
         return t.data_ptr()
-    raise FlashLoopError(fn, -1, f"{name}: a contiguous {dtype} tensor of at least {n} elements on cuda:{dev}, "
-                                 f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    raise FlashLoopError(fn, -1, f"{name}: a contiguous {dtype} tensor of at least {n} elements{f' in rows of {row}' if row > 1 else ''} "
+                                 f"on cuda:{dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _rows(fn, name, t, shape, dtype, dev, written=False):
@@ -440,7 +450,7 @@ def _launch(fn, dev, stream, *args):
 def flashloop_paged_plan(params, kv_lens, new_lens, free_pages, n_free, block_table, cu, kv_lens_out, slot_map,
                          positions, n_free_out, err_word, stream=None):
     """Block tables, slot maps, positions and packed starts of the tokens that the requests
-    append (see the header).  int32 tensors; block_table [batch, max_blocks] and n_free_out,
+    append (see the header).  int32 tensors; block_table [batch, max_blocks] (or flat) and n_free_out,
     kv_lens_out, cu [batch + 1], slot_map and positions [max_tokens] are written."""
     rc = _fastcall.plan(params, kv_lens, new_lens, free_pages, n_free, block_table, cu, kv_lens_out, slot_map, positions,
                         n_free_out, err_word, stream)
@@ -451,7 +461,7 @@ def flashloop_paged_plan(params, kv_lens, new_lens, free_pages, n_free, block_ta
     return _launch(fn, dev, stream, ctypes.byref(p), _vec(fn, "kv_lens", kv_lens, B, i32, dev),
                    _vec(fn, "new_lens", new_lens, B, i32, dev),
                    _vec(fn, "free_pages", free_pages, 0, i32, dev), free_pages.numel(), _vec(fn, "n_free", n_free, 1, i32, dev),
-                   _vec(fn, "block_table", block_table, B * p.max_blocks, i32, dev),
+                   _vec(fn, "block_table", block_table, B * p.max_blocks, i32, dev, p.max_blocks),
                    _vec(fn, "cu", cu, B + 1, i32, dev), _vec(fn, "kv_lens_out", kv_lens_out, B, i32, dev),
                    _vec(fn, "slot_map", slot_map, T, i32, dev), _vec(fn, "positions", positions, T, i32, dev),
                    _vec(fn, "n_free_out", n_free_out, 1, i32, dev), _vec(fn, "err_word", err_word, 1, i32, dev))
@@ -488,7 +498,7 @@ def flashloop_prompt_attn(params, q, k, v, cu, o, lse, err_word, stream=None):
     orr = _rows(fn, "o", o, qs, dt, dev, True)
     return _launch(fn, dev, stream, ctypes.byref(p), ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr),
                    _vec(fn, "cu", cu, p.batch + 1, torch.int32, dev), ctypes.byref(orr),
-                   None if lse is None else _vec(fn, "lse", lse, p.n_heads * p.max_tokens, torch.float32, dev),
+                   None if lse is None else _vec(fn, "lse", lse, p.n_heads * p.max_tokens, torch.float32, dev, p.max_tokens),
                    _vec(fn, "err_word", err_word, 1, torch.int32, dev))
 
 
@@ -512,10 +522,10 @@ def flashloop_paged_attn(params, q, k_cache, v_cache, block_table, kv_lens, cu, 
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise FlashLoopError(fn, -1, "workspace: contiguous, on the tensors' device")
     return _launch(fn, dev, stream, ctypes.byref(p), ctypes.byref(qr), ctypes.byref(kc), ctypes.byref(vc),
-                   _vec(fn, "block_table", block_table, p.batch * p.max_blocks, i32, dev),
+                   _vec(fn, "block_table", block_table, p.batch * p.max_blocks, i32, dev, p.max_blocks),
                    _vec(fn, "kv_lens", kv_lens, p.batch, i32, dev), _vec(fn, "cu", cu, p.batch + 1, i32, dev),
                    ctypes.byref(orr),
-                   None if lse is None else _vec(fn, "lse", lse, p.n_heads * p.max_tokens, torch.float32, dev),
+                   None if lse is None else _vec(fn, "lse", lse, p.n_heads * p.max_tokens, torch.float32, dev, p.max_tokens),
                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                    _vec(fn, "err_word", err_word, 1, i32, dev))
 
