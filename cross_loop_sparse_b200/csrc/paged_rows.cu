@@ -294,8 +294,9 @@ __device__ __forceinline__ bool pr_item(const PrArgs& a, const PrItem& s, uint8_
   }
   cp_async_wait<0>();
 
+  const bool look = !AGAIN && ncols > free_cols;
   bool odd = false;
-  if (!AGAIN && ncols > free_cols) {
+  if (look) {
     float t[4] = {0.f, 0.f, 0.f, 0.f};  // zeros, or NaN
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -336,7 +337,8 @@ __device__ __forceinline__ bool pr_item(const PrArgs& a, const PrItem& s, uint8_
         *reinterpret_cast<float2*>(d + n * 8) = x;
       }
     }
-  if (__syncthreads_or(odd)) return true;
+  if (!look) __syncthreads();
+  else if (__syncthreads_or(odd)) return true;
   for (int i = threadIdx.x; i < C::kRows * (DH / 4); i += kPrThreads) {
     const int r = i / (DH / 4), c = (i % (DH / 4)) * 4;
     if (r0 + r >= rows) break;
