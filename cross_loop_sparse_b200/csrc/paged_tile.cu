@@ -17,10 +17,11 @@
 // or of a page, or one box a page where pages are smaller.  Boxes of pages
 // behind the request's end start outside the tensor and fill with zeros.  The
 // V rows that some row of the pair does not see are looked over before the tile
-// is handed on, since 0 * NaN would reach that row: those behind the request's end are
+// is handed on, since 0 * NaN would reach that row: those that no row sees are
 // cleared, and what is not finite of the others is set to zero and added to the
-// numerators of the rows that see it when they are written back (4200 us against
-// 4180 without for a prompt of 32768 tokens x 16 heads).
+// numerators of the rows that see it when they are written back.  A prompt of 32768
+// tokens x 16 heads takes 4156 us with that and 4124 without, 20 prompts of 700
+// tokens x 32 heads 137 and 130; by the row warps instead of the loads' 144.
 // TMEM (512 columns): N_A, N_B, then the tiles' 128-column scores; the P of a
 // 64-column half is written over the half's first 32 score columns and feeds
 // that half's P.V from TMEM.  The next tile's scores of a half are issued right
@@ -280,6 +281,11 @@ __device__ __forceinline__ int pt_seen_by_all(const PtItem& it, const PgArgs& g)
   return max(0, it.L - it.n + g.by_g(it.r0) + 1);
 }
 
+// Columns that its last row sees.
+__device__ __forceinline__ int pt_seen_by_some(const PtItem& it, const PgArgs& g) {
+  return it.L - it.n + g.by_g(min(it.r0 + kPtPair, it.n * g.G) - 1) + 1;
+}
+
 // Column tiles of the item that tile x (0 = A, 1 = B) reads, from t0 on.
 __device__ __forceinline__ int pt_mine(const PtItem& it, const PgArgs& g, int x) {
   const int first = it.r0 + x * kPtRows;
@@ -436,8 +442,9 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const int next = i + 1 < nt ? page_of(t + 1) : 0;
         const int col = t * kPtCols + lane * box;
         const int y = g.table ? (col & ((1 << g.shift) - 1)) : it.q0 + col;
-        const int live = it.L - t * kPtCols;  // tokens of the tile before the request's end
-        const int from = max(0, pt_seen_by_all(it, g) - t * kPtCols);  // first that some row does not see
+        // the tile's rows that all of the pair's rows see, and those that some do
+        const int from = max(0, pt_seen_by_all(it, g) - t * kPtCols);
+        const int held = min(pt_seen_by_some(it, g) - t * kPtCols, kPtCols);
         for (int kv = 0; kv < 2; ++kv, ++seq) {
           const int slot = seq % C::kStages;
           const uint32_t ph = (seq / C::kStages) & 1;
@@ -461,7 +468,6 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
               break;
             }
             ++tails;
-            const int held = min(live, kPtCols);
             PgFinite<BF> finite;
 #pragma unroll 4
             for (int j = from * 8 + lane; j < held * 8; j += 32) {
@@ -480,11 +486,9 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
               // the item's place is the write-back's until it has read it, which waits for this tile's product
               if (lane == 0) items[k & 1].odd = 1;
             }
-            for (int j = lane; j < (kPtCols - live) * 8; j += 32) {
+            for (int j = held * 8 + lane; j < kPtCols * 8; j += 32) {
 #pragma unroll
-              for (int c = 0; c < DH / 64; ++c)
-                *reinterpret_cast<uint4*>(st + c * C::kChunk + (live + (j >> 3)) * 128 + (j & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
+              for (int c = 0; c < DH / 64; ++c) *reinterpret_cast<uint4*>(st + c * C::kChunk + j * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -604,33 +608,37 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     constexpr int kPieces = DH / 8;
     const int quarter = warp - kPtWarpQ, row = quarter * 32 + lane;
     // To the numerators of tile x in TMEM: the values that the loads' warp took out of the item's V tiles.
+    // One channel at a time: the write-back is longer where this takes more registers.
     auto add_odd = [&](const PtItem& it, int x, uint32_t nbase) {
       const int r = it.r0 + x * kPtRows + row;
-      const int end = r < it.n * g.G ? min(it.L - it.n + g.by_g(r) + 1, it.t1 * kPtCols) : 0;
-      const int first = max(pt_seen_by_all(it, g), it.t0 * kPtCols);
+      const int end = r < it.n * g.G ? it.L - it.n + g.by_g(r) + 1 : 0;  // columns that the row sees
+      const int stop = min(pt_seen_by_some(it, g), it.t1 * kPtCols);
 #pragma unroll 1
-      for (int cc = 0; cc < DH; cc += 16) {
-        uint32_t w[16];
-        tmem_ld16(nbase + cc, w);
-        tmem_wait_ld();
-#pragma unroll 1
-        for (int j = first; j < end; ++j) {
-          const uint16_t* v = g.v.p + it.h * g.v.sh + cc;
-          if (g.table) {
-            const int page = g.table[(size_t)it.b * g.max_blocks + (j >> g.shift)];
-            if (page < 0 || page >= g.n_pages) continue;
-            v += page * g.v.sp + (j & ((1 << g.shift) - 1)) * g.v.st;
-          } else {
-            v += (long long)(it.q0 + j) * g.v.st;
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (pg_not_finite<BF>(v[e])) w[e] = __float_as_uint(__uint_as_float(w[e]) + pg_unpack2<BF>(v[e]).x);
+      for (int j = max(pt_seen_by_all(it, g), it.t0 * kPtCols); j < stop; ++j) {
+        const uint16_t* v = g.v.p + it.h * g.v.sh;
+        if (g.table) {
+          const int page = g.table[(size_t)it.b * g.max_blocks + (j >> g.shift)];
+          if (page < 0 || page >= g.n_pages) continue;
+          v += page * g.v.sp + (j & ((1 << g.shift) - 1)) * g.v.st;
+        } else {
+          v += (long long)(it.q0 + j) * g.v.st;
         }
-        __syncwarp();
-        tmem_st16(nbase + cc, w);
+#pragma unroll 1
+        for (int c = lane; c < DH; c += 32) {
+          unsigned odd = __ballot_sync(0xffffffffu, pg_not_finite<BF>(v[c]));
+          while (odd) {
+            const int e = c - lane + __ffs(odd) - 1;
+            odd &= odd - 1;
+            uint32_t w;
+            tmem_ld1(nbase + e, w);
+            tmem_wait_ld();
+            if (j < end) w = __float_as_uint(__uint_as_float(w) + pg_unpack2<BF>(v[e]).x);
+            __syncwarp();
+            tmem_st1(nbase + e, w);
+            tmem_wait_st();
+          }
+        }
       }
-      tmem_wait_st();
     };
     // The rows of item k, once both tiles' P.V and 1 / z are there: o = N / z, or N to scratch.
     auto write_back = [&](uint32_t k) -> bool {
