@@ -56,15 +56,30 @@ def _compile(src: str, verbose: bool, force: bool) -> str:
     return obj
 
 
+def fastcall_target() -> str:
+    """What _fastcall.so, which uses torch's and the interpreter's C++ and C interfaces, has to be built for."""
+    import torch
+    return f"torch {torch.__version__}, C++11 ABI {int(torch.compiled_with_cxx11_abi())}, {sys.implementation.cache_tag}"
+
+
+def fastcall_fits() -> bool:
+    """Whether there is a _fastcall.so for this torch and interpreter: the file says what it was built for."""
+    if not os.path.exists(FAST):
+        return False
+    with open(FAST, "rb") as f:
+        return fastcall_target().encode() + b"\0" in f.read()
+
+
 def _build_fastcall(force: bool) -> None:
     src = os.path.join(CSRC, "fastcall.cpp")
     newest_dep = max(os.path.getmtime(f) for f in [src, os.path.join(INCLUDE, "flashloop.h")])
-    if not force and os.path.exists(FAST) and os.path.getmtime(FAST) >= newest_dep:
+    if not force and fastcall_fits() and os.path.getmtime(FAST) >= newest_dep:
         return
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f'-DFLASHLOOP_BUILT_FOR="{fastcall_target()}"', "-I", INCLUDE]
     for inc in (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(cuda, "include")):
         cmd += ["-isystem", inc]

@@ -218,5 +218,8 @@ PyMODINIT_FUNC PyInit__fastcall() {
                                   {"attn", fast(attn), METH_FASTCALL, nullptr},
                                   {nullptr, nullptr, 0, nullptr}};
   static PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
-  return PyModule_Create(&module);
+  PyObject* m = PyModule_Create(&module);
+  // the build and the import look for this text in the file
+  if (m && PyModule_AddStringConstant(m, "built_for", FLASHLOOP_BUILT_FOR) != 0) Py_CLEAR(m);
+  return m;
 }

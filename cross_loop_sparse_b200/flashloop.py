@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import warnings
 from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 import torch
@@ -416,11 +417,23 @@ def _paged_dtype(fn, p):
 
 
 # The same marshalling in C++ for the plain case, tensors on the current device; None where it leaves
-# a call to the functions below.
+# a call to the functions below.  It is built for one torch and interpreter; the functions below serve
+# any, with 10 us of host time a call where it takes 4.
+class _NoFastcall:
+    plan = write = prompt = attn = staticmethod(lambda *args: None)
+    bind = plan
+
+
+from .build import fastcall_fits  # noqa: E402  (behind the library, without which there is nothing to build for)
+
 try:
+    if not fastcall_fits():
+        raise ImportError("missing, or built for another torch or interpreter")
     from . import _fastcall
 except ImportError as exc:
-    raise ImportError(f"{_PKG}/_fastcall.so: build it with `python -m cross_loop_sparse_b200.build`") from exc
+    _fastcall = _NoFastcall
+    warnings.warn(f"{_PKG}/_fastcall.so: {exc}. The many-request calls take longer on the host; build it with "
+                  "`python -m cross_loop_sparse_b200.build`", stacklevel=2)
 _fastcall.bind(*(ctypes.cast(getattr(_lib, fn), c_void_p).value for fn in (
     "flashloop_paged_plan", "flashloop_paged_kv_write", "flashloop_prompt_attn", "flashloop_paged_attn")))
 
