@@ -11,6 +11,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <algorithm>
 #include <cstring>
 
 #include "flashloop.h"
@@ -132,8 +133,7 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Call c(a[0], a[1], a[12]);
     const long long B = c.p.batch, T = c.p.max_tokens;
     int32_t *kv = c.ints(a[1], B), *add = c.ints(a[2], B), *stack = c.ints(a[3], 0), *n_free = c.ints(a[4], 1);
-    const long long capacity = Call::tensor(a[3]).numel();
-    if (capacity > 0x7fffffffll) throw NotPlain();
+    const long long capacity = std::min<long long>(Call::tensor(a[3]).numel(), 0x7fffffff);  // at most n_pages of it count
     int32_t *table = c.table(a[5]), *cu = c.ints(a[6], B + 1), *kv_out = c.ints(a[7], B);
     int32_t *slot = c.ints(a[8], T), *pos = c.ints(a[9], T), *left = c.ints(a[10], 1), *err = c.ints(a[11], 1);
     return without_gil([&] {

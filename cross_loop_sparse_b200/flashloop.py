@@ -473,7 +473,7 @@ def flashloop_paged_plan(params, kv_lens, new_lens, free_pages, n_free, block_ta
     B, T = max(p.batch, 0), max(p.max_tokens, 0)
     return _launch(fn, dev, stream, ctypes.byref(p), _vec(fn, "kv_lens", kv_lens, B, i32, dev),
                    _vec(fn, "new_lens", new_lens, B, i32, dev),
-                   _vec(fn, "free_pages", free_pages, 0, i32, dev), free_pages.numel(), _vec(fn, "n_free", n_free, 1, i32, dev),
+                   _vec(fn, "free_pages", free_pages, 0, i32, dev), min(free_pages.numel(), 2 ** 31 - 1), _vec(fn, "n_free", n_free, 1, i32, dev),
                    _vec(fn, "block_table", block_table, B * p.max_blocks, i32, dev, p.max_blocks),
                    _vec(fn, "cu", cu, B + 1, i32, dev), _vec(fn, "kv_lens_out", kv_lens_out, B, i32, dev),
                    _vec(fn, "slot_map", slot_map, T, i32, dev), _vec(fn, "positions", positions, T, i32, dev),

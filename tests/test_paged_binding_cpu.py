@@ -92,3 +92,37 @@ def test_marshalling_is_built_again_for_another_torch(tmp_path, monkeypatch):
     assert len(ran) == 1 and build.fastcall_fits() and any(build.fastcall_target() in a for a in ran[0])
     build._build_fastcall(False)
     assert len(ran) == 1
+
+
+class Fake:
+    """What the Python marshalling asks of a tensor, for sizes that need no memory."""
+    dtype, device = torch.int32, "cuda:0"
+
+    def __init__(self, *shape):
+        self.shape = shape
+
+    def get_device(self):
+        return 0
+
+    def numel(self):
+        n = 1
+        for d in self.shape:
+            n *= d
+        return n
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 4096
+
+
+@pytest.mark.parametrize("entries,want", [(7, 7), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1), (2 ** 32 + 1, 2 ** 31 - 1)])
+def test_a_stack_of_any_size_keeps_its_capacity(monkeypatch, entries, want):
+    """The library takes the capacity in 32 bits: a longer buffer must not wrap to a short or negative one."""
+    seen = []
+    monkeypatch.setattr(F, "_launch", lambda fn, dev, stream, *args: seen.append(args) or 0)
+    p = F.PagedParams.make(2, 4, 2, 1, 1, 64, 16, 10, 3)
+    F.flashloop_paged_plan(p, Fake(2), Fake(2), Fake(entries), Fake(1), Fake(2, 3), Fake(3), Fake(2), Fake(4), Fake(4), Fake(1), Fake(1))
+    types = F._lib.flashloop_paged_plan.argtypes
+    assert len(seen[0]) == len(types) - 1 and types[4](seen[0][4]).value == want
