@@ -95,6 +95,16 @@ __device__ __forceinline__ void pg_mma(float (&d)[4], const uint32_t (&a)[4], ui
   else mma_f16(d, a, b0, b1);
 }
 
+// The running reference of the exponentials p = 2^(s - m) is raised when a score exceeds it by kRise,
+// to kLift below that score.  A probability is then at most 2^kRise, and the row's largest at least
+// 2^kLift.  In fp16, whose numbers end at 2^16 and lose bits below 2^-14, the lift keeps all bits of
+// probabilities down to 2^-21 of the largest, where they would go at 2^-14 without: a row whose
+// first key draws nearly all of its weight to a value of zero is the sum of those.  bf16 has the range.
+template <int BF>
+struct PgRef {
+  static constexpr float kLift = BF ? 0.f : 7.f, kRise = 8.f + kLift;
+};
+
 // Values that are not finite.  A row's probability of a column that it does not see is zero, and zero
 // times infinity or NaN would reach the row through the product.  So the values that are not finite
 // of columns that some row of a tile does not see are zeros in the product, and are added to the

@@ -8,8 +8,7 @@
 // columns in stages of 64, 16 to each of its four warps; a warp keeps its own
 // ring of asynchronous copies, running maximum, sum and numerator over its
 // columns, so that nothing synchronises the warps until they are joined at
-// the end.  With m the running reference (log2 units, raised only when a
-// score exceeds it by 8, which bounds a probability by 2^8),
+// the end.  With m the running reference (log2 units, see PgRef),
 //   p = 2^(s - m), z = sum p, N = sum p v, o = N / z, lse = (m + log2 z) ln 2.
 // Scores, sums and N are float32.  The matrix product takes p in the values'
 // type.  Up to 16 packed rows, what that rounding drops is multiplied with V too,
@@ -34,7 +33,6 @@ namespace fl {
 
 constexpr int kPrThreads = 128;
 constexpr int kPrCols = 64;  // columns a stage, 16 a warp
-constexpr float kPrRescale = 8.f;
 
 template <int DH, int MT>
 struct PrCfg {
@@ -236,8 +234,10 @@ __device__ __forceinline__ bool pr_item(const PrArgs& a, const PrItem& s, uint8_
         mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 1));
         mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 2)) * g.scale_log2;
       }
-      const bool up0 = mx[0] > m[mt][0] + kPrRescale, up1 = mx[1] > m[mt][1] + kPrRescale;
+      const bool up0 = mx[0] > m[mt][0] + PgRef<BF>::kRise, up1 = mx[1] > m[mt][1] + PgRef<BF>::kRise;
       if (__any_sync(0xffffffffu, up0 || up1)) {
+        mx[0] -= PgRef<BF>::kLift;
+        mx[1] -= PgRef<BF>::kLift;
         const float f0 = up0 ? ex2(m[mt][0] - mx[0]) : 1.f;
         const float f1 = LO == 1 ? f0 : up1 ? ex2(m[mt][1] - mx[1]) : 1.f;
         if (up0) m[mt][0] = mx[0];

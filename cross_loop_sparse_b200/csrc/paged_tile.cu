@@ -6,7 +6,7 @@
 // read the same keys.  Work item: one request, key head and pair of 128-row
 // tiles A, B, over a range of 128-column tiles; A and B share every K / V
 // tile.  Per row, with s the scores in log2 units and m a reference raised
-// only when a score exceeds it by 8,
+// only by leaps (see PgRef),
 //   p = 2^(s - m), z = sum p, N = sum p v, o = N / z, lse = (m + log2 z) ln 2;
 // scores, z and N in float32, p rounded to the values' type because the
 // matrix product takes one type for both operands.
@@ -67,7 +67,6 @@ constexpr int kPtPair = 2 * kPtRows;
 constexpr int kPtCols = 128;
 constexpr int kPtThreads = 512;
 constexpr int kPtWarpQ = 8, kPtWarpTma = 12, kPtWarpMma = 13, kPtWarpSched = 15;
-constexpr float kPtRescale = 8.f;
 constexpr int kPtRegsRows = 192, kPtRegsRest = 64;  // of the 65536 registers: 256 threads of each
 constexpr int kPtReaders = 15;   // arrivals that free a work item's slot: 8 + 4 + 1 + 2 warps
 constexpr int kPtMinUnits = 4;   // units a block takes at least when the line is cut
@@ -820,11 +819,11 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           };
           exps();
           const float mx = fmaxf(max32(s0), max32(s1)) * g.scale_log2;
-          const bool need = mx > m_ref + kPtRescale;
+          const bool need = mx > m_ref + PgRef<BF>::kRise;
           if (__any_sync(0xffffffffu, need)) {
-            // raise it: z and the numerator so far scale by 2^(m_ref - mx) once the last P.V has
+            // raise it: z and the numerator so far scale by 2^(old - new) once the last P.V has
             // completed; the scores that were issued behind it say so
-            const float f = need ? ex2(m_ref - mx) : 1.f;
+            const float f = need ? ex2(m_ref - (mx - PgRef<BF>::kLift)) : 1.f;
             uint64_t* behind = hf == 0 ? &s_full[2 * x + 1] : t + 1 < my ? &s_full[2 * x] : &pv0_done[x];
             const uint32_t phase = hf == 0 ? u : t + 1 < my ? u + 1 : full;
             if ((t > 0 || hf > 0) && !wait(behind, phase & 1)) break;
@@ -840,7 +839,7 @@ pg_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
               }
             }
             z *= f;
-            if (need) m_ref = mx;
+            if (need) m_ref = mx - PgRef<BF>::kLift;
             exps();
           }
           tmem_st32(at, pk);

@@ -130,3 +130,34 @@ TILE_PAGED = [
 @pytest.mark.parametrize("total,new,H,Hk,dh,page,dt,layout", TILE_PAGED)
 def test_paged_tiles_see_their_own_columns_values(total, new, H, Hk, dh, page, dt, layout):
     paged_case(total, new, H, Hk, dh, page, dt, layout, wide(H), True)
+
+
+def sink_tolerance(q, k, v, first, scale):
+    """The bounds of `attention` for fp16 with the probabilities' absolute step at 2^-32 of the largest: rounded at
+    2^-25 or better (half a step of its smallest numbers), with the largest at 2^7 or more."""
+    o, _, tol, _ = attention(q, k, v, first, scale)
+    each = v.double().abs().sum(0).repeat_interleave(q.shape[1] // v.shape[1], 0)[None]
+    return o, tol - 2.0 ** -25 * each + 2.0 ** -32 * each
+
+
+@pytest.mark.parametrize("gap", [6, 10, 14, 16, 18])  # nats between the first key's score and the others'
+@pytest.mark.parametrize("new,H,extra", [(1, 4, False), (1, 16, False), (3, 8, False), (150, 8, True)])  # both roundings of few rows, 24 rows, tiles
+def test_small_probabilities_of_fp16_count(gap, new, H, extra):
+    """A first key that draws nearly all weight to a value of zero: the result is the many small probabilities'."""
+    L, dh, page = 6000, 128, 64
+    n_pages = -(-L // page)
+    kc, vc = torch.zeros(n_pages, page, 1, dh, dtype=HF, device="cuda"), (4 + randn(gen(gap), n_pages, page, 1, dh)).to(HF)
+    kc[0, 0, 0, 0], vc[0, 0] = gap, 0.0
+    T = new + (wide(H) if extra else 0)
+    q = torch.zeros(T, H, dh, dtype=HF, device="cuda")
+    q[:, :, 0] = 1.0
+    p = F.PagedParams.make(batch=1, max_tokens=T, max_new=new, n_heads=H, n_kv_heads=1, head_dim=dh, page_size=page, n_pages=n_pages, max_blocks=n_pages, dtype=HF, scale=1.0)
+    assert tiles(p, True) == extra
+    table, o, lse, err = ints([list(range(n_pages))]), torch.zeros_like(q), torch.zeros(H, T, device="cuda"), ints([0])
+    F.flashloop_paged_attn(p, q, kc, vc, table, ints([L]), ints([0, new]), o, lse, workspace(p), err)
+    k, v = gather(kc, table[0], L), gather(vc, table[0], L)
+    want, tol = sink_tolerance(q[:new], k, v, L - new, 1.0)
+    _, l, _, lt = attention(q[:new], k, v, L - new, 1.0)
+    off = (o[:new].double() - want).abs()
+    assert (off <= tol).all(), ((off / want.abs().clamp(min=1e-30)).median().item(), (off - tol).max().item())
+    assert ((lse[:, :new].double() - l).abs() <= lt).all() and err.item() == 0
