@@ -16,17 +16,12 @@ namespace fl {
 constexpr int kPjThreads = 512;
 constexpr int kPjWarps = kPjThreads / 32;
 constexpr int kPjRows = 64;           // rows of a tile item a block takes
-constexpr int kPjParts = 2 * kPgSms;  // an item has at most a part a block of the few-row kernel
 
 struct PjArgs {
   PgArgs g;
-  const PgCut* tile_cuts;  // [kPgSms], four blocks each
-  const PgCut* row_cuts;   // [row_blocks], a block each, the first ones
-  int row_blocks;
-  const float2* tile_mz;
-  const float2* row_mz;
-  const float4* tile_n;
-  const float4* row_n;
+  const PgCut* cuts;  // of the tile kernel, four blocks each, or of the few-row kernel, a block each
+  const float2* mz;
+  const float4* n;
 };
 
 // The weight of a part in a row: none if it saw nothing of it (it has no numerator in scratch either).
@@ -49,40 +44,38 @@ __device__ __forceinline__ void pj_axpy(float4& acc, float w, const float4& x) {
   acc.w += w * x.w;
 }
 
-template <int DH, int BF>
+// FEW: the parts are the few-row kernel's.
+template <int DH, int BF, int FEW>
 __global__ void __launch_bounds__(kPjThreads) pg_join_kernel(PjArgs a) {
   constexpr int kC4 = DH / 4;
-  // weights [row][part]: 32 rows of up to kPjParts parts, or 64 of up to kPgSms
-  constexpr int kWeights = kPgFewRows * (kPjParts + 1) > kPjRows * (kPgSms + 1) ? kPgFewRows * (kPjParts + 1)
-                                                                             : kPjRows * (kPgSms + 1);
-  __shared__ float s_w[kWeights];
-  __shared__ float s_inv[kPjRows];  // 1 / z
-  __shared__ float4 s_acc[kPjThreads];
+  constexpr int kRows = FEW ? kPgFewRows : kPjRows, kSlotRows = FEW ? kPgFewRows : kPgTileRows;
+  constexpr int kShare = kSlotRows / kRows;                // blocks an item
+  constexpr int kParts = FEW ? 2 * kPgSms : kPgSms;        // at most a part a block
+  __shared__ float s_w[kRows * (kParts + 1)];              // weights [row][part]
+  __shared__ float s_inv[kRows];                           // 1 / z
+  __shared__ float4 s_acc[FEW ? kPjThreads : 1];
   pg_wait_for_launch_before();
   const PgArgs& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool few = (int)blockIdx.x < a.row_blocks;
-  const int tile = blockIdx.x - a.row_blocks;
-  const PgCut c = few ? a.row_cuts[blockIdx.x] : a.tile_cuts[tile / (kPgTileRows / kPjRows)];
+  const PgCut c = a.cuts[blockIdx.x / kShare];
   if (c.parts < 2) return;
-  const int slot_rows = few ? kPgFewRows : kPgTileRows;
-  const int first = few ? 0 : (tile % (kPgTileRows / kPjRows)) * kPjRows;
-  const int live = min(min(c.n * g.G - c.r0, slot_rows) - first, kPjRows);
+  const int first = (blockIdx.x % kShare) * kRows;
+  const int live = min(min(c.n * g.G - c.r0, kSlotRows) - first, kRows);
   if (live <= 0) return;
   const int pitch = c.parts | 1;
   // part i > 0 lies in its block's first slot
   auto slot = [&](int i) { return (size_t)(i == 0 ? c.slot0 : (c.slot0 & ~1) + 2 * i); };
-  const float2* mz_of = (few ? a.row_mz : a.tile_mz) + first;
+  const float2* mz_of = a.mz + first;
   // rows' weights: `lanes` lanes a row, as many as there are parts or a warp
   const int lanes = c.parts > 16 ? 32 : c.parts > 8 ? 16 : c.parts > 4 ? 8 : 4;
   for (int r0 = 0; r0 < live; r0 += kPjWarps * (32 / lanes)) {
     const int r = r0 + warp * (32 / lanes) + lane / lanes, k0 = lane % lanes;
     const bool on = r < live;
     float m = -INFINITY, z = 0.f;
-    for (int k = k0; on && k < c.parts; k += lanes) m = fmaxf(m, __ldcg(mz_of + slot(k) * slot_rows + r).x);
+    for (int k = k0; on && k < c.parts; k += lanes) m = fmaxf(m, __ldcg(mz_of + slot(k) * kSlotRows + r).x);
     for (int o = lanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     for (int k = k0; on && k < c.parts; k += lanes) {
-      const float2 mz = __ldcg(mz_of + slot(k) * slot_rows + r);
+      const float2 mz = __ldcg(mz_of + slot(k) * kSlotRows + r);
       const float w = pj_weight(mz, m);
       s_w[r * pitch + k] = w;
       if (w != 0.f) z += w * mz.y;
@@ -96,12 +89,12 @@ __global__ void __launch_bounds__(kPjThreads) pg_join_kernel(PjArgs a) {
     }
   }
   __syncthreads();
-  if (!few) {
+  if (!FEW) {
     // numerators [column / 4][row]: four of a thread at a time
     constexpr int kPer = kPjRows * kC4 / kPjThreads;
     const int r = threadIdx.x % kPjRows, q0 = threadIdx.x / kPjRows;
     if (r >= live) return;
-    const float4* n = a.tile_n + (size_t)q0 * kPgTileRows + first + r;
+    const float4* n = a.n + (size_t)q0 * kPgTileRows + first + r;
     float4 acc[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -131,7 +124,7 @@ __global__ void __launch_bounds__(kPjThreads) pg_join_kernel(PjArgs a) {
       const int k1 = c.parts * (group + 1) / groups;
 #pragma unroll 8
       for (int k = c.parts * group / groups; k < k1; ++k)
-        pj_axpy(acc, s_w[r * pitch + k], __ldcg(a.row_n + (slot(k) * kPgFewRows + r) * kC4 + c4));
+        pj_axpy(acc, s_w[r * pitch + k], __ldcg(a.n + (slot(k) * kPgFewRows + r) * kC4 + c4));
     }
     s_acc[threadIdx.x] = acc;
     __syncthreads();
@@ -144,12 +137,17 @@ __global__ void __launch_bounds__(kPjThreads) pg_join_kernel(PjArgs a) {
 }
 
 int launch_pg_join(const PgArgs& g, int dh, int bf16, const PgScratch& ws, cudaStream_t stream) {
-  PjArgs a{g, ws.tile_cuts, ws.row_cuts, ws.row_cuts ? 2 * kPgSms : 0, ws.tile_mz, ws.row_mz, ws.tile_n, ws.row_n};
-  const int blocks = a.row_blocks + (ws.tile_cuts ? kPgSms * (kPgTileRows / kPjRows) : 0);
-  if (blocks == 0) return FLASHLOOP_OK;
+  if (!ws.tile_cuts && !ws.row_cuts) return FLASHLOOP_OK;
+  const bool few = ws.row_cuts != nullptr;  // a call's scratch is one kernel's
+  const PjArgs a = few ? PjArgs{g, ws.row_cuts, ws.row_mz, ws.row_n} : PjArgs{g, ws.tile_cuts, ws.tile_mz, ws.tile_n};
+  const int blocks = few ? 2 * kPgSms : kPgSms * (kPgTileRows / kPjRows);
   auto go = [&](auto kernel) { return pg_launch_early(kernel, dim3(blocks), kPjThreads, 0, stream, a); };
-  if (dh == 128) return bf16 ? go(pg_join_kernel<128, 1>) : go(pg_join_kernel<128, 0>);
-  return bf16 ? go(pg_join_kernel<64, 1>) : go(pg_join_kernel<64, 0>);
+  if (few) {
+    if (dh == 128) return bf16 ? go(pg_join_kernel<128, 1, 1>) : go(pg_join_kernel<128, 0, 1>);
+    return bf16 ? go(pg_join_kernel<64, 1, 1>) : go(pg_join_kernel<64, 0, 1>);
+  }
+  if (dh == 128) return bf16 ? go(pg_join_kernel<128, 1, 0>) : go(pg_join_kernel<128, 0, 0>);
+  return bf16 ? go(pg_join_kernel<64, 1, 0>) : go(pg_join_kernel<64, 0, 0>);
 }
 
 }  // namespace fl
