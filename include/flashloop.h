@@ -501,7 +501,9 @@ const char* flashloop_status_string(int status);
  *
  * Keys and values that are not finite reach the rows that see their column, and
  * no others.  An infinite value is the row's result there, or NaN beside one of the
- * other sign; with a probability too small for the values' type it may be either. */
+ * other sign; where its probability underflows it may be that, NaN or left out.
+ *
+ * o may be q itself, and overlaps nothing else that a call reads. */
 #define FLASHLOOP_DTYPE_BF16 0
 #define FLASHLOOP_DTYPE_FP16 1
 #define FLASHLOOP_DTYPE_FP32 2

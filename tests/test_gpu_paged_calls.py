@@ -45,3 +45,56 @@ def test_wider_tables_and_turned_sums_are_refused(way, monkeypatch):
     plan(table)
     prompt(want)
     assert err.item() == 0
+
+
+@pytest.mark.parametrize("n", [2, 300])  # few-row kernel, tile kernel
+def test_capture_over_two_streams(n):
+    """Early launches where a kernel follows one of its own stream and one of another: writes and attention of two
+    pools side by side, each step on the other stream than the last, joined and forked in one graph."""
+    B, H, Hk, dh, page, steps = 3, 8, 2, 64, 16, 6
+    width = steps * n // page + 2
+
+    def inputs(seed):
+        p = F.PagedParams.make(batch=B, max_tokens=B * n, max_new=n, n_heads=H, n_kv_heads=Hk, head_dim=dh, page_size=page, n_pages=B * width, max_blocks=width)
+        return dict(p=p, q0=randn(gen(seed), B * n, H, dh, dtype=BF), q=torch.empty(B * n, H, dh, dtype=BF, device="cuda"), o=torch.empty(B * n, H, dh, dtype=BF, device="cuda"),
+                    kv=[ints([0] * B) for _ in range(2)], new=ints([n] * B), free=ints(list(range(B * width))), left=[ints([B * width]), ints([0])], start=ints([B * width]), none=ints([0] * B),
+                    table=ints([[-1] * width] * B), cu=ints([0] * (B + 1)), slots=ints([0] * B * n), pos=ints([0] * B * n), err=ints([0]), ws=workspace(p),
+                    kc=torch.zeros(B * width, page, Hk, dh, dtype=BF, device="cuda"), vc=torch.zeros(B * width, page, Hk, dh, dtype=BF, device="cuda"))
+
+    def reset(c):
+        c["q"].copy_(c["q0"])
+        c["kv"][0].copy_(c["none"])
+        c["left"][0].copy_(c["start"])
+
+    def step(c, i):
+        a, b = i % 2, (i + 1) % 2
+        F.flashloop_paged_plan(c["p"], c["kv"][a], c["new"], c["free"], c["left"][a], c["table"], c["cu"], c["kv"][b], c["slots"], c["pos"], c["left"][b], c["err"])
+        F.flashloop_paged_kv_write(c["p"], c["q"][:, :Hk], c["q"][:, Hk:2 * Hk], c["slots"], c["kc"], c["vc"], c["err"])
+        F.flashloop_paged_attn(c["p"], c["q"], c["kc"], c["vc"], c["table"], c["kv"][b], c["cu"], c["o"], None, c["ws"], c["err"])
+        F.flashloop_prompt_attn(c["p"], c["o"], c["o"][:, 2:4], c["o"][:, 4:6], c["cu"], c["q"], None, c["err"])
+
+    pools = [inputs(1), inputs(2)]
+    want = []
+    for c in pools:
+        reset(c)
+        for i in range(steps):
+            step(c, i)
+            torch.cuda.synchronize()
+        want.append([c[x].clone() for x in ("q", "o", "kc", "vc")])
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        for c in pools:
+            reset(c)
+        for i in range(steps):
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                step(pools[i % 2], i)
+            step(pools[1 - i % 2], i)
+            main.wait_stream(side)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for c, w in zip(pools, want):
+            assert all(torch.equal(c[x], y) for x, y in zip(("q", "o", "kc", "vc"), w)) and c["err"].item() == 0
+        assert want[0][0].isfinite().all()
