@@ -10,7 +10,7 @@
 //
 // write: a copy with a gathered destination, bound by HBM.  A thread moves one
 // 16-byte piece of a row's K and of its V, so both loads are in flight at once:
-// 32768 rows of 16 heads x 128, float32 to bf16, in 127 us, 6.3 TB/s.
+// 32768 rows of 16 heads x 128, float32 to bf16, in 124 us, 6.5 TB/s.
 #include "paged.cuh"
 
 namespace fl {

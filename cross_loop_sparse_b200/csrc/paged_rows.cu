@@ -18,8 +18,9 @@
 // bound the kernel, p is rounded, which makes the error sqrt(2) times as large.
 //
 // Bound by HBM: a column costs 4 * head_dim bytes and few instructions (8 contexts
-// of 32768 tokens, 16 heads of 128: 308 us, 7.0 TB/s; with 17 to 32 packed rows 4.4
-// TB/s, where eight warps an SM cannot hide two tiles' products).  With
+// of 32768 tokens, 16 heads of 128: 306 to 314 us by card, 6.8 to 7.0 TB/s; with 32
+// packed rows a key head 100 us for 537 MB, 5.4 TB/s, where eight warps an SM cannot
+// hide two tiles' products).  With
 // scratch, the stages of all requests and key heads are one line that is cut
 // into equal lengths, one a block and two blocks an SM, so that requests of any
 // mix of lengths load the SMs alike; what a border cuts leaves float32 N, m and z
@@ -39,8 +40,8 @@ struct PrCfg {
   static constexpr int kRows = 16 * MT;
   static constexpr int kTile = 16 * DH * 2;  // bytes of a warp's K (or V) slice of a stage
   // 128 KB an SM on their way are enough for HBM, and more are slower: 8 contexts of 32768 tokens
-  // take 308 us with 2 stages of 16 heads of 128 and 320 with 3, 98 us with 3 stages of 8 heads
-  // of 64, 99 with 2, 102 with 4 and 104 with 6
+  // take 308 us with 2 stages of 16 heads of 128 and 320 with 3 on one card, 98 us with 3 stages of
+  // 8 heads of 64, 99 with 2, 102 with 4 and 104 with 6
   static constexpr int kStages = DH == 128 ? 2 : 3;
   static constexpr int kWarpRing = kStages * 2 * kTile;
   static constexpr int kPitch = DH + 8;  // floats, of the joined numerators

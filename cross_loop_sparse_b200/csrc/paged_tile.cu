@@ -30,7 +30,7 @@
 // would do (it reads the queries for half as many columns, and shared memory
 // gives 128 bytes a clock), but 128-wide ones, at their full rate, leave the rows
 // waiting for a whole P.V and score MMA a tile: 4.1 ms against 3.5 ms for a
-// prompt of 32768 tokens x 16 heads.
+// prompt of 32768 tokens x 16 heads on a cool card (at its power cap this one takes 4.2).
 //
 // Roles (16 warps): 0-3 / 4-7 rows of tile A / B, one thread a row; 8-11
 // queries of the next item and write-back of the last, while the row warps take

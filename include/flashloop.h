@@ -581,8 +581,10 @@ int flashloop_paged_kv_write(const flashloop_paged_params* p, const flashloop_ro
  *   o_i = sum_j e^(s_j - lse) v_j.
  * k and v are rows of n_kv_heads heads packed as q is.  float32 scores and
  * sums; the probabilities enter the product with V rounded to the values'
- * type, with a second product of what that drops where a request has at most 16
- * rows times heads a key head.  lse: float32 [n_heads, max_tokens], or NULL.  The page fields of
+ * type.  Where a request has at most 16 rows times heads a key head, a second
+ * product adds what that drops, in calls whose bounds (max_tokens, max_new,
+ * max_blocks and the heads) are small enough for the kernel of few rows: all
+ * with max_new * n_heads / n_kv_heads <= 32.  lse: float32 [n_heads, max_tokens], or NULL.  The page fields of
  * params are not used. */
 int flashloop_prompt_attn(const flashloop_paged_params* p, const flashloop_rows* q, const flashloop_rows* k,
                           const flashloop_rows* v, const int32_t* cu, const flashloop_rows* o, float* lse,
