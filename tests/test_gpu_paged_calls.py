@@ -98,3 +98,32 @@ def test_capture_over_two_streams(n):
         for c, w in zip(pools, want):
             assert all(torch.equal(c[x], y) for x, y in zip(("q", "o", "kc", "vc"), w)) and c["err"].item() == 0
         assert want[0][0].isfinite().all()
+
+
+def test_plan_without_requests_or_rows():
+    """No requests: every slot is padding and the stack stays; no rows: the lengths stay."""
+    for B, T in ((0, 9), (3, 0), (0, 0)):
+        p = F.PagedParams.make(batch=B, max_tokens=T, max_new=1, n_heads=1, n_kv_heads=1, head_dim=64, page_size=16, n_pages=6, max_blocks=2)
+        kv, new, table = ints([5] * B), ints([0] * B), ints([[3, -1]] * B).view(B, 2)
+        cu, kv_out, slots, pos, left, err = ints([9] * (B + 1)), ints([9] * B), ints([9] * T), ints([9] * T), ints([9]), ints([0])
+        F.flashloop_paged_plan(p, kv, new, ints([4, 1]), ints([2]), table, cu, kv_out, slots, pos, left, err)
+        assert cu.tolist() == [0] * (B + 1) and kv_out.tolist() == [5] * B and left.tolist() == [2] and err.item() == 0
+        assert slots.tolist() == [-1] * T and pos.tolist() == [0] * T and table.tolist() == [[3, -1]] * B
+
+
+@pytest.mark.parametrize("kind", ["none", "object", "handle"])
+def test_every_way_to_name_a_stream(kind):
+    """The current stream, a stream object and a raw handle: the call runs there."""
+    p, q, kc, vc, table, cu = paged_inputs([300, 40], [2, 1], 4, 2, 64, 16, BF, "thd", 0)
+    want, got, err, ws = torch.zeros_like(q), torch.zeros_like(q), ints([0]), workspace(p)
+    F.flashloop_paged_attn(p, q, kc, vc, table, ints([300, 40]), ints(cu), want, None, ws, err)
+    kv, cus = ints([300, 40]), ints(cu)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    if kind == "none":
+        with torch.cuda.stream(s):
+            F.flashloop_paged_attn(p, q, kc, vc, table, kv, cus, got, None, ws, err)
+    else:
+        F.flashloop_paged_attn(p, q, kc, vc, table, kv, cus, got, None, ws, err, stream=s if kind == "object" else s.cuda_stream)
+    s.synchronize()
+    assert torch.equal(got, want) and err.item() == 0

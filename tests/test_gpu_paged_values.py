@@ -161,3 +161,26 @@ def test_small_probabilities_of_fp16_count(gap, new, H, extra):
     off = (o[:new].double() - want).abs()
     assert (off <= tol).all(), ((off / want.abs().clamp(min=1e-30)).median().item(), (off - tol).max().item())
     assert ((lse[:, :new].double() - l).abs() <= lt).all() and err.item() == 0
+
+
+@pytest.mark.parametrize("n,H,Hk,dh,dt,extra", [(40, 4, 2, 128, BF, False), (150, 8, 1, 64, HF, False), (300, 4, 2, 128, HF, True), (520, 2, 2, 64, BF, True)])
+@pytest.mark.parametrize("what", ["key", "query"])
+def test_keys_and_queries_that_are_not_finite(n, H, Hk, dh, dt, extra, what):
+    """A key reaches the rows that see its column, a query its own row and head, also within a tile."""
+    g, T, at = gen(n), n + (wide(H) if extra else 0), n * 2 // 3
+    q, k, v = randn(g, T, H, dh, dtype=dt), randn(g, T, Hk, dh, dtype=dt), randn(g, T, Hk, dh, dtype=dt)
+    p = F.PagedParams.make(batch=1, max_tokens=T, max_new=n, n_heads=H, n_kv_heads=Hk, head_dim=dh, dtype=dt)
+    assert tiles(p, False) == extra
+    want, l, tol, lt = attention(q[:n], k[:n], v[:n], 0, dh ** -0.5)
+    hit = torch.zeros(n, H, dtype=torch.bool, device="cuda")
+    if what == "key":
+        k[at, Hk - 1, 7] = math.nan
+        hit[at:, H - H // Hk:] = True
+    else:
+        q[at, 1, 3], q[at + 5, 0, 9] = math.nan, math.inf
+        hit[at, 1], hit[at + 5, 0] = True, True
+    o, lse, err = torch.full_like(q, 7.0), torch.full((H, T), 7.0, device="cuda"), ints([0])
+    F.flashloop_prompt_attn(p, q, k, v, ints([0, n]), o, lse, err)
+    assert o[:n][hit].isnan().all() and not lse[:, :n].T[hit].isfinite().any()
+    assert (((o[:n].double() - want).abs() - tol)[~hit] <= 0).all() and (((lse[:, :n].T.double() - l.T).abs() - lt.T)[~hit] <= 0).all()
+    assert (o[n:] == 7).all() and err.item() == 0
