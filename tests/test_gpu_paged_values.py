@@ -184,3 +184,18 @@ def test_keys_and_queries_that_are_not_finite(n, H, Hk, dh, dt, extra, what):
     assert o[:n][hit].isnan().all() and not lse[:, :n].T[hit].isfinite().any()
     assert (((o[:n].double() - want).abs() - tol)[~hit] <= 0).all() and (((lse[:, :n].T.double() - l.T).abs() - lt.T)[~hit] <= 0).all()
     assert (o[n:] == 7).all() and err.item() == 0
+
+
+@pytest.mark.parametrize("lens,H,Hk,dh,tile", [([6000, 900], 8, 8, 128, True), ([4000], 16, 1, 64, True), ([60] * 9, 8, 8, 128, False)])
+def test_nothing_but_values_that_are_not_finite(lens, H, Hk, dh, tile):
+    """Every value taken out and put back: no wait runs out, and every row is what it sees."""
+    cu, g = starts(lens), gen(1)
+    T = cu[-1]
+    q, k = randn(g, T, H, dh, dtype=BF), randn(g, T, Hk, dh, dtype=BF)
+    v = torch.full((T, Hk, dh), math.inf, dtype=BF, device="cuda")
+    v[..., ::2], v[..., 1::4] = math.nan, -math.inf
+    p = F.PagedParams.make(batch=len(lens), max_tokens=T, max_new=max(lens), n_heads=H, n_kv_heads=Hk, head_dim=dh)
+    assert tiles(p, False) == tile
+    o, err = torch.zeros_like(q), ints([0])
+    F.flashloop_prompt_attn(p, q, k, v, ints(cu), o, None, err)
+    assert o[..., ::2].isnan().all() and (o[..., 1::4] == -math.inf).all() and (o[..., 3::4] == math.inf).all() and err.item() == 0
